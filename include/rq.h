@@ -328,6 +328,68 @@ rq_status rq_gemm_wq(const uint16_t *x, int64_t M, int64_t K, const void *codes,
                      rq_stream_t stream);
 
 /*
+ * rq_tmix_scan, rq_tmix_scan_bwd, rq_tmix_step -- the gated linear recurrence
+ * between the R/K/V projections and the O projection of an RWKV-7 time-mix
+ * block.  (The pages name the model family and its projections; the recurrence
+ * is the family's published time-mix formula.)  Per head of 64 channels, with
+ * a state S[64 (value i), 64 (key j)] in fp32, for every token t:
+ *   w_t = exp(-e^{-1/2} sigmoid(d_t))                       the decay, per key
+ *   S_t = S_{t-1} diag(w_t) + (S_{t-1} a_t) b_t^T + v_t k_t^T
+ *   y_t = S_t r_t
+ * (In the model a = -kappa, b = kappa * gate with a normalised key kappa; here
+ * a and b are free.)  All arithmetic is fp32; y is rounded once.
+ *
+ * r, d, k, v, a, b: [T, H, 64] device, 16-byte aligned, of one type dtype
+ * (RQ_OUT_F32 or RQ_OUT_F16, else RQ_ERR_RANGE), tokens ld elements apart
+ * (ld >= 64 H, ld % 8 == 0, else RQ_ERR_SHAPE), so that they may be columns of
+ * one larger matrix.  y (and every gradient): [T, H, 64] contiguous, same type,
+ * 16-byte aligned.
+ * seq_start: int32 [S + 1] device: sequence i is the tokens seq_start[i] ..
+ * seq_start[i + 1] - 1; a sequence may be empty (its state is passed on).
+ * Tokens outside every sequence are not read and their outputs are left as
+ * they were.  Offsets must not fall; a pair that falls or leaves 0 .. T sets
+ * dev_status (optional, caller-zeroed device int) to RQ_ERR_RANGE and its
+ * sequence is skipped.
+ * state_in: fp32 [*, H, 64, 64] device or NULL (zeros).  state_out: the same,
+ * or NULL (dropped); it may be state_in itself.  slots: int32 [S] device or
+ * NULL: which state sequence i uses, 0 <= slot < n_slots (n_slots >= 1 states
+ * in both); a negative slot means none (zeros in, nothing out); one that is
+ * too large does too, and sets dev_status to RQ_ERR_RANGE.  NULL: state i.
+ * Two sequences of one call must not share a slot when state_out is given.
+ * ckpt: NULL, or rq_tmix_ckpt_bytes(T, S, H) bytes for rq_tmix_scan_bwd: the
+ * state before every 16th token of each sequence.
+ * 0 <= T < 2^30, S >= 1, H >= 1, (T / 16 + S) * H < 2^29, else RQ_ERR_SHAPE.
+ * With T = 0 the [T, ...] pointers may be NULL.
+ *
+ * rq_tmix_scan_bwd -- gradients of the same call: dy [T, H, 64] and dstate_out
+ * (gradient of the final states, fp32 [S, H, 64, 64], NULL: zeros) give dr ..
+ * db and dstate_in (gradient of the initial states, NULL: dropped).  Same
+ * inputs as the forward call, with its ckpt.  work: rq_tmix_ckpt_bytes bytes.
+ * States are by sequence (no slots).  Deterministic.
+ *
+ * rq_tmix_step -- one token for each of B sequences: r .. b and y [B, H, 64],
+ * states and slots as above.  B >= 1.
+ *
+ * No call allocates; all are asynchronous on `stream`.
+ */
+size_t rq_tmix_ckpt_bytes(int64_t T, int64_t S, int64_t H);
+rq_status rq_tmix_scan(const void *r, const void *d, const void *k, const void *v, const void *a,
+                       const void *b, int64_t T, int64_t H, int64_t ld, int dtype,
+                       const int32_t *seq_start, int64_t S, const float *state_in, float *state_out,
+                       const int32_t *slots, int64_t n_slots, void *y, float *ckpt, int *dev_status,
+                       rq_stream_t stream);
+rq_status rq_tmix_scan_bwd(const void *r, const void *d, const void *k, const void *v, const void *a,
+                           const void *b, int64_t T, int64_t H, int64_t ld, int dtype,
+                           const int32_t *seq_start, int64_t S, const float *ckpt, const void *dy,
+                           const float *dstate_out, float *dstate_in, void *dr, void *dd, void *dk,
+                           void *dv, void *da, void *db, float *work, int *dev_status,
+                           rq_stream_t stream);
+rq_status rq_tmix_step(const void *r, const void *d, const void *k, const void *v, const void *a,
+                       const void *b, int64_t B, int64_t H, int64_t ld, int dtype,
+                       const float *state_in, float *state_out, const int32_t *slots,
+                       int64_t n_slots, void *y, int *dev_status, rq_stream_t stream);
+
+/*
  * rq_gemv_wq_noalloc -- rq_gemv_wq for callers that cannot have a library
  * allocate device memory.  (The pages describe no such variant; it exists for
  * this library's users.)

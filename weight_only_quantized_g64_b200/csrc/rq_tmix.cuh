@@ -1,0 +1,158 @@
+// rq_tmix.cuh -- what the kernels of the time-mix recurrence share: packed
+// fp32 arithmetic, the decay, element loads, the sequence table.
+//
+// Per head, with a 64 x 64 fp32 state S (rows i: value, columns j: key),
+//   w_t = exp(-e^{-1/2} sigmoid(d_t))
+//   S_t = S_{t-1} diag(w_t) + (S_{t-1} a_t) b_t^T + v_t k_t^T,   y_t = S_t r_t.
+// Every row of S evolves by itself: its update needs the row, the five key
+// vectors of the token and one value v_i.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "rq_internal.h"
+
+namespace rq {
+
+constexpr int kHead = 64;                    // channels of a head
+constexpr int kTmixChunk = 16;               // tokens between two stored states (training)
+constexpr float kDecay = 0.60653065971263342f;   // e^{-1/2}
+
+struct TmixArgs {
+    const void* in[6];                       // r, d, k, v, a, b: [T, H, 64], rows ld elements apart
+    const void* dy;                          // backward: [T, H, 64]
+    void* out[6];                            // forward: y; backward: dr, dd, dk, dv, da, db
+    const float* state_in;                   // [*, H, 64, 64] or NULL
+    float* state_out;                        // [*, H, 64, 64] or NULL
+    const int32_t* slots;                    // [S] state of each sequence, or NULL: its own index
+    const int32_t* seq_start;                // [S + 1]
+    float* ckpt;                             // forward states before each chunk, or NULL
+    float* gckpt;                            // backward: gradient of the state after each chunk
+    int* status;
+    int64_t T, ld, n_slots;
+    int S, H;
+};
+
+// ------------------------------------------------------- packed fp32 pairs --
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// ---------------------------------------------------------------- elements --
+// Eight consecutive elements, 16-byte aligned (fp16: one load, fp32: two).
+struct Raw8 {
+    uint4 u[2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8 load8(const T* p) {
+    Raw8 r;
+    r.u[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    if constexpr (sizeof(T) == 4) r.u[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void cvt8(const Raw8& r, float* f) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 a = *reinterpret_cast<const float4*>(&r.u[0]);
+        const float4 b = *reinterpret_cast<const float4*>(&r.u[1]);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+        const __half2* h = reinterpret_cast<const __half2*>(&r.u[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = __half22float2(h[i]);
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+    if constexpr (sizeof(T) == 4) return __ldg(reinterpret_cast<const float4*>(p));
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = v;
+    } else {
+        const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                                  *reinterpret_cast<const uint32_t*>(&b));
+    }
+}
+template <typename T>
+__device__ __forceinline__ float to_f32(T v) {
+    if constexpr (sizeof(T) == 4) return v;
+    else return __half2float(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_f32(float v) {
+    if constexpr (sizeof(T) == 4) return v;
+    else return __float2half_rn(v);
+}
+
+// ------------------------------------------------------------------- decay --
+__device__ __forceinline__ float decay_gate(float d) { return 1.f / (1.f + expf(-d)); }
+__device__ __forceinline__ float decay_log(float d) { return -kDecay * decay_gate(d); }
+// w - 1: the update w S = S + (w - 1) S then rounds S once, and a decay near 1
+// keeps its distance from 1 over thousands of steps (w itself, rounded to 24
+// bits, would be off by up to 2^-25 in every step, in the same direction).
+__device__ __forceinline__ float decay_m1(float d) { return expm1f(decay_log(d)); }
+
+// --------------------------------------------------------------- sequences --
+// Tokens [lo, hi) of sequence i; false (and a status) for offsets that are
+// not 0 <= lo <= hi <= T.
+__device__ __forceinline__ bool sequence_of(const TmixArgs& p, int i, int& lo, int& hi) {
+    lo = p.seq_start[i];
+    hi = p.seq_start[i + 1];
+    if (lo >= 0 && hi >= lo && hi <= p.T) return true;
+    if (p.status != nullptr && threadIdx.x == 0) atomicMax(p.status, RQ_ERR_RANGE);
+    return false;
+}
+// State of sequence i, -1 for none (a negative slot, or one out of range,
+// which also sets the status).
+__device__ __forceinline__ int64_t state_of(const TmixArgs& p, int i) {
+    if (p.slots == nullptr) return i;
+    const int s = p.slots[i];
+    if (s < p.n_slots) return s < 0 ? -1 : s;
+    if (p.status != nullptr && threadIdx.x == 0) atomicMax(p.status, RQ_ERR_RANGE);
+    return -1;
+}
+// First stored state of a sequence: sequences of len tokens have
+// ceil(len / chunk) of them, and lo / chunk + i leaves room for each.
+__device__ __forceinline__ int64_t ckpt_base(int lo, int i) { return lo / kTmixChunk + i; }
+
+cudaError_t launch_tmix_scan(const TmixArgs& a, bool half, bool reverse, cudaStream_t s);
+cudaError_t launch_tmix_step(const TmixArgs& a, bool half, cudaStream_t s);
+cudaError_t launch_tmix_chunks_bwd(const TmixArgs& a, bool half, cudaStream_t s);
+
+}  // namespace rq

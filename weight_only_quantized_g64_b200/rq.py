@@ -7,6 +7,7 @@ librq.so is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -80,6 +81,14 @@ def lib():
     L.rq_gemv_p8_g16.restype = i32
     L.rq_gemv_p4a_g32.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp]
     L.rq_gemv_p4a_g32.restype = i32
+    L.rq_tmix_ckpt_bytes.argtypes = [i64, i64, i64]
+    L.rq_tmix_ckpt_bytes.restype = ctypes.c_size_t
+    L.rq_tmix_scan.argtypes = [vp] * 6 + [i64, i64, i64, i32, vp, i64, vp, vp, vp, i64, vp, vp, vp, vp]
+    L.rq_tmix_scan.restype = i32
+    L.rq_tmix_scan_bwd.argtypes = [vp] * 6 + [i64, i64, i64, i32, vp, i64] + [vp] * 13
+    L.rq_tmix_scan_bwd.restype = i32
+    L.rq_tmix_step.argtypes = [vp] * 6 + [i64, i64, i64, i32, vp, vp, vp, i64, vp, vp, vp]
+    L.rq_tmix_step.restype = i32
     L.rq_set_pdl.argtypes = [i32]
     L.rq_set_pdl.restype = i32
     L.rq_set_decode_kernel.argtypes = [i32]
@@ -316,6 +325,160 @@ def rkv_fused(x: torch.Tensor, wr, wk, wv, N: int, bits: int, ys=None, stream=No
                               _p(wv[0]), _p(wv[1]), _p(ys[0]), _p(ys[1]), _p(ys[2]),
                               _stream(stream)), "rq_rkv_fused")
     return ys
+
+
+HEAD = 64
+
+
+def _placed(fn):
+    """The call runs, and allocates, on its first tensor's device and on the
+    given stream (default: that device's current one)."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda or (
+                stream is None and first.device.index == torch.cuda.current_device()):
+            return fn(first, *args, **kw)
+        with torch.cuda.device(first.device), torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _need(ok: bool, what: str, status: int = ERR_SHAPE):
+    if not ok:
+        raise RQError(status, what)
+
+
+def _tensor(call: str, name: str, t, dtype, shape, like=None):
+    """t is a contiguous tensor of this type and shape (and on like's device)."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise RQError(ERR_SHAPE, f"{call}: {name} must be a contiguous {dtype} {tuple(shape)}, "
+                                 f"not {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    if like is not None and t.device != like.device:
+        raise RQError(ERR_SHAPE, f"{call}: {name} is on {t.device}, not on {like.device}")
+
+
+def _on_gpu(call: str, t):
+    if not t.is_cuda:
+        raise RQError(ERR_SHAPE, f"{call}: the tensors must be on a CUDA device, not on {t.device}")
+
+
+_REAL = {torch.float32: OUT_F32, torch.float16: OUT_F16}
+
+
+def _heads(call: str, names: str, tensors):
+    """Checks the [T, H, 64] inputs of one call -> (T, H, row stride)."""
+    x = tensors[0]
+    _need(x.dim() == 3 and x.shape[2] == HEAD, f"{call}: {names[0]} must be [T, H, {HEAD}], not {tuple(x.shape)}")
+    _need(x.dtype in _REAL, f"{call}: {names[0]} must be float32 or float16, not {x.dtype}", ERR_RANGE)
+    T, H = x.shape[0], x.shape[1]
+    ld = x.stride(0) if T > 1 else H * HEAD
+    for n, t in zip(names, tensors):
+        if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+            raise RQError(ERR_SHAPE, f"{call}: {n} must be {x.dtype} {tuple(x.shape)} on {x.device} like {names[0]}, "
+                                     f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+        if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != HEAD) or (T > 1 and t.stride(0) != ld)):
+            raise RQError(ERR_SHAPE, f"{call}: {n} must have strides ({ld}, {HEAD}, 1), not {t.stride()}")
+    return T, H, ld
+
+
+def _states(call: str, x, S: int, H: int, state, state_out, slots, dev_status):
+    """Checks states and slots -> the number of states."""
+    n = S
+    for name, t in (("state", state), ("state_out", state_out)):
+        if t is not None:
+            if slots is not None and t.dim() == 4:
+                n = t.shape[0]
+            _tensor(call, name, t, torch.float32, (n, H, HEAD, HEAD), x)
+    if slots is not None:
+        _tensor(call, "slots", slots, torch.int32, (S,), x)
+        _need(state is not None or state_out is not None, f"{call}: slots without a state")
+        _need(state is None or state_out is None or state.shape == state_out.shape,
+              f"{call}: state and state_out must have the same shape")
+    if dev_status is not None:
+        _tensor(call, "dev_status", dev_status, torch.int32, dev_status.shape, x)
+    return n
+
+
+def tmix_ckpt(x: torch.Tensor, S: int) -> torch.Tensor:
+    """Memory for the states that tmix_scan keeps for tmix_scan_bwd: x [T, H, 64]
+    one of the call's inputs, S its number of sequences."""
+    n = int(lib().rq_tmix_ckpt_bytes(x.shape[0], S, x.shape[1]))
+    _need(n > 0, "rq_tmix_ckpt_bytes")
+    return torch.empty(n // 4, dtype=torch.float32, device=x.device)
+
+
+@_placed
+def tmix_scan(r, d, k, v, a, b, seq_start, state=None, state_out=None, slots=None, y=None, ckpt=None,
+              dev_status=None):
+    """The time-mix recurrence over sequences: r, d, k, v, a, b fp32 or fp16
+    [T, H, 64] (rows may be columns of a wider matrix); seq_start int32 [S + 1]
+    device.  state fp32 [S, H, 64, 64] (None: zeros), or a pool of states with
+    slots int32 [S].  Returns (y, state_out); state_out may be state itself, is
+    allocated when not given, and for a pool must be given."""
+    c = "rq_tmix_scan"
+    T, H, ld = _heads(c, "rdkvab", (r, d, k, v, a, b))
+    S = seq_start.numel() - 1
+    _tensor(c, "seq_start", seq_start, torch.int32, (max(S, 1) + 1,), r)
+    n = _states(c, r, S, H, state, state_out, slots, dev_status)
+    if ckpt is not None:
+        _tensor(c, "ckpt", ckpt, torch.float32, (lib().rq_tmix_ckpt_bytes(T, S, H) // 4,), r)
+    if y is not None:
+        _tensor(c, "y", y, r.dtype, (T, H, HEAD), r)
+    _on_gpu(c, r)
+    if y is None:
+        y = torch.empty((T, H, HEAD), dtype=r.dtype, device=r.device)
+    if state_out is None and slots is None:
+        state_out = torch.empty((S, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
+    _check(lib().rq_tmix_scan(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), T, H, ld, _REAL[r.dtype], _p(seq_start), S,
+                              _p(state), _p(state_out), _p(slots), n, _p(y), _p(ckpt), _p(dev_status),
+                              _stream()), c)
+    return y, state_out
+
+
+@_placed
+def tmix_scan_bwd(r, d, k, v, a, b, seq_start, ckpt, dy, dstate_out=None, grads=None, dstate=None,
+                  dev_status=None):
+    """Gradients of tmix_scan (called with this ckpt and without slots) from dy
+    [T, H, 64] and dstate_out [S, H, 64, 64] (None: zeros).  Returns ((dr, dd,
+    dk, dv, da, db), dstate)."""
+    c = "rq_tmix_scan_bwd"
+    T, H, ld = _heads(c, "rdkvab", (r, d, k, v, a, b))
+    S = seq_start.numel() - 1
+    _tensor(c, "seq_start", seq_start, torch.int32, (max(S, 1) + 1,), r)
+    _tensor(c, "ckpt", ckpt, torch.float32, (lib().rq_tmix_ckpt_bytes(T, S, H) // 4,), r)
+    _tensor(c, "dy", dy, r.dtype, (T, H, HEAD), r)
+    _states(c, r, S, H, dstate_out, dstate, None, dev_status)
+    for i, g in enumerate(grads or ()):
+        _tensor(c, f"grads[{i}]", g, r.dtype, (T, H, HEAD), r)
+    _on_gpu(c, r)
+    if grads is None:
+        grads = tuple(torch.empty((T, H, HEAD), dtype=r.dtype, device=r.device) for _ in range(6))
+    if dstate is None:
+        dstate = torch.empty((S, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
+    work = torch.empty_like(ckpt)
+    _check(lib().rq_tmix_scan_bwd(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), T, H, ld, _REAL[r.dtype],
+                                  _p(seq_start), S, _p(ckpt), _p(dy), _p(dstate_out), _p(dstate),
+                                  *(_p(g) for g in grads), _p(work), _p(dev_status), _stream()), c)
+    return tuple(grads), dstate
+
+
+@_placed
+def tmix_step(r, d, k, v, a, b, state=None, state_out=None, slots=None, y=None, dev_status=None):
+    """One token of the time-mix recurrence for each of B sequences: r .. b fp32
+    or fp16 [B, H, 64]; state as in tmix_scan.  Returns (y, state_out)."""
+    c = "rq_tmix_step"
+    B, H, ld = _heads(c, "rdkvab", (r, d, k, v, a, b))
+    n = _states(c, r, B, H, state, state_out, slots, dev_status)
+    if y is not None:
+        _tensor(c, "y", y, r.dtype, (B, H, HEAD), r)
+    _on_gpu(c, r)
+    if y is None:
+        y = torch.empty((B, H, HEAD), dtype=r.dtype, device=r.device)
+    if state_out is None and slots is None:
+        state_out = torch.empty((B, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
+    _check(lib().rq_tmix_step(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), B, H, ld, _REAL[r.dtype], _p(state),
+                              _p(state_out), _p(slots), n, _p(y), _p(dev_status), _stream()), c)
+    return y, state_out
 
 
 def set_pdl(enable: bool):
