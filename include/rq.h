@@ -328,6 +328,75 @@ rq_status rq_gemm_wq(const uint16_t *x, int64_t M, int64_t K, const void *codes,
                      rq_stream_t stream);
 
 /*
+ * rq_lora_add -- low-rank adapters of many requests beside a shared projection
+ * (the weight is quantized and shared; the adapters stay fp16, as the model
+ * card keeps its low-rank matrices in full precision, "Format & loading
+ * (important)").  For every token m with a = ids[m]:
+ *   out[m, n] = epi( y[m, n] + scale[a] * sum_{r < ranks[a]} B[a, n, r] t[r] ),
+ *   t[r] = sum_k A[a, r, k] x[m, k];
+ * a token with a negative id has no adapter: out[m, n] = epi(y[m, n]); an id
+ * that is not below L counts as none too and sets dev_status (optional,
+ * caller-zeroed device int) to RQ_ERR_RANGE.  Sums are fp32 (the products of
+ * fp16 values exact, t kept to at least 22 bits); out is rounded once.
+ *
+ * x: fp16 [M, K].  A: fp16 [L, R, K].  B: fp16 [L, N, R].  ids: int32 [M].
+ * ranks: int32 [L] or NULL (all R); values above R count as R, below 0 as 0;
+ * what A and B hold behind an adapter's rank does not enter any result.
+ * scale: fp32 [L] or NULL (1).  y, out: [M, N] of dtype (RQ_OUT_F32 or
+ * RQ_OUT_F16); out may be y itself, else they must not overlap.  epilogue:
+ * RQ_EPI_NONE or RQ_EPI_RELU_SQ (the squared ReLU then comes here, not in the
+ * product before).  Bad dtype or epilogue: RQ_ERR_RANGE.  K % 8 == 0, R % 8 ==
+ * 0, 8 <= R <= RQ_MAX_LORA_RANK, 1 <= M <= 4194240, any N >= 1, else
+ * RQ_ERR_SHAPE.  work: rq_lora_work_bytes(M, K, R) bytes, 16-byte aligned
+ * (0 bytes, NULL allowed, for M <= RQ_MAX_DECODE_M).  Tokens of one request
+ * need not be neighbours, but tiles of neighbours are faster.  Deterministic;
+ * asynchronous on `stream`; allocates nothing.
+ */
+#define RQ_MAX_LORA_RANK 128
+size_t rq_lora_work_bytes(int64_t M, int64_t K, int64_t R);
+rq_status rq_lora_add(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A, const uint16_t *B,
+                      int64_t L, int64_t R, const int32_t *ids, const int32_t *ranks,
+                      const float *scale, const void *y, void *out, int64_t N, int dtype, int epilogue,
+                      float *work, int *dev_status, rq_stream_t stream);
+
+/*
+ * rq_norm_residual -- the step between two projections, in one pass:
+ *   u  = (Norm_post(y) + add) * act(gate)
+ *   h' = h + alpha * u                                    -> h_out
+ *   x  = Norm_pre(h')                                     -> x (fp16)
+ * Every part may be absent.  After a time-mix recurrence: post the norm of each
+ * head (post_group 64), add the bonus, gate the block's gate, and x feeds the O
+ * projection; between blocks: y a projection's output, h the residual stream,
+ * alpha its scale, and x feeds the next projections; with both norms, the form
+ * that norms a block before and after.
+ *
+ * y, add, gate: [M, D] of dtype (RQ_OUT_F32 or RQ_OUT_F16), rows ld_* elements
+ * apart; h, h_out: [M, D] of the same dtype, contiguous; x: fp16 [M, D].
+ * add, gate, h, alpha: NULL when absent.  h_out may be h itself; h_out or x may
+ * be NULL, not both.  Norms: RQ_NORM_NONE, RQ_NORM_LAYER ((v - mean) /
+ * sqrt(var + eps), var the mean square about the mean), RQ_NORM_RMS (v /
+ * sqrt(mean square + eps)), over the whole row or, for post, over post_group
+ * channels (0 or D: the row; else 8, 16, .. 256, dividing D), then * weight + bias
+ * (fp32 [D] each, or NULL).  gate_act: RQ_GATE_IDENTITY, RQ_GATE_SIGMOID,
+ * RQ_GATE_SILU.  alpha: fp32 [D].  All arithmetic is fp32; Norm_pre reads h'
+ * before it is rounded.  D % 64 == 0, 64 <= D <= 16384, M >= 1, strides >= D
+ * and multiples of 8, else RQ_ERR_SHAPE; a bad dtype, norm, act or a negative
+ * eps: RQ_ERR_RANGE; pointers 16-byte aligned.  Asynchronous on `stream`.
+ */
+#define RQ_NORM_NONE 0
+#define RQ_NORM_LAYER 1
+#define RQ_NORM_RMS 2
+#define RQ_GATE_IDENTITY 0
+#define RQ_GATE_SIGMOID 1
+#define RQ_GATE_SILU 2
+rq_status rq_norm_residual(const void *y, int64_t ld_y, int64_t M, int64_t D, int dtype, int post,
+                           int64_t post_group, const float *post_weight, const float *post_bias,
+                           float eps_post, const void *add, int64_t ld_add, const void *gate,
+                           int64_t ld_gate, int gate_act, const void *h, const float *alpha, int pre,
+                           const float *pre_weight, const float *pre_bias, float eps_pre, void *h_out,
+                           uint16_t *x, rq_stream_t stream);
+
+/*
  * rq_tmix_scan, rq_tmix_scan_bwd, rq_tmix_step -- the gated linear recurrence
  * between the R/K/V projections and the O projection of an RWKV-7 time-mix
  * block.  (The pages name the model family and its projections; the recurrence

@@ -107,3 +107,82 @@ def test_tmix_binding_refuses(L):
     # good arguments, but on the host
     refused(rq.ERR_SHAPE, rq.tmix_scan, *xs, seq)
     refused(rq.ERR_SHAPE, rq.tmix_step, *xs, state=torch.zeros(4, 2, 64, 64))
+
+
+def lora_args(**kw):
+    a = dict(x=FAKE, M=40, K=64, A=FAKE, B=FAKE, L=2, R=16, ids=FAKE, ranks=None, scale=None, y=FAKE, out=FAKE, N=33,
+             dtype=0, epi=0, work=FAKE, status=None, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+def test_lora_argument_errors(L):
+    f = L.rq_lora_add
+    for bad in (dict(dtype=2), dict(dtype=-1), dict(epi=2), dict(epi=-1)):
+        assert f(*lora_args(**bad)) == rq.ERR_RANGE, bad
+    for bad in (dict(M=0), dict(M=4194241), dict(K=0), dict(K=12), dict(N=0), dict(N=1 << 31), dict(L=0), dict(R=0),
+                dict(R=12), dict(R=136)):
+        assert f(*lora_args(**bad)) == rq.ERR_SHAPE, bad
+    for n in ("x", "A", "B", "ids", "y", "out", "work"):
+        assert f(*lora_args(**{n: None})) == rq.ERR_NULL, n
+    for n in ("x", "A", "B", "y", "out", "work"):
+        assert f(*lora_args(**{n: FAKE + 8})) == rq.ERR_ALIGN, n
+    for n in ("ids", "ranks", "scale", "status"):
+        assert f(*lora_args(**{n: FAKE + 2})) == rq.ERR_ALIGN, n
+    assert L.rq_lora_work_bytes(32, 4096, 64) == 0
+    assert L.rq_lora_work_bytes(33, 4096, 64) % (33 * 64 * 4) == 0 < L.rq_lora_work_bytes(33, 4096, 64)
+    assert L.rq_lora_work_bytes(33, 4096, 12) == 0
+
+
+def test_lora_binding_refuses(L):
+    x, A, B = torch.zeros(4, 64).half(), torch.zeros(2, 8, 64).half(), torch.zeros(2, 10, 8).half()
+    ids, y = torch.zeros(4, dtype=torch.int32), torch.zeros(4, 10)
+    refused(rq.ERR_RANGE, rq.lora_add, x, A, B, ids, y.double())
+    refused(rq.ERR_SHAPE, rq.lora_add, x.float(), A, B, ids, y)
+    refused(rq.ERR_SHAPE, rq.lora_add, x, A[:, :, :32], B, ids, y)
+    refused(rq.ERR_SHAPE, rq.lora_add, x, A, B.mT, ids, y)
+    refused(rq.ERR_SHAPE, rq.lora_add, x, A, B[:1], ids, y)
+    refused(rq.ERR_SHAPE, rq.lora_add, x, A, B, ids.long(), y)
+    refused(rq.ERR_SHAPE, rq.lora_add, x, A, B, ids[:3], y)
+    refused(rq.ERR_SHAPE, rq.lora_add, x, A, B, ids, y[:, :9])
+    refused(rq.ERR_SHAPE, rq.lora_add, x, A, B, ids, y, out=y.half())
+    refused(rq.ERR_SHAPE, rq.lora_add, x, A, B, ids, y, scale=torch.zeros(3))
+    refused(rq.ERR_SHAPE, rq.lora_add, x, A, B, ids, y, ranks=torch.zeros(2))
+    refused(rq.ERR_SHAPE, rq.lora_add, x, A, B, ids, y)          # on the host
+
+
+def norm_args(**kw):
+    a = dict(y=FAKE, ldy=128, M=3, D=128, dtype=0, post=1, group=64, pw=FAKE, pb=FAKE, ep=1e-5, add=FAKE, lda=128,
+             gate=FAKE, ldg=128, act=1, h=FAKE, alpha=FAKE, pre=2, w=FAKE, b=FAKE, e=1e-5, ho=FAKE, x=FAKE, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+def test_norm_argument_errors(L):
+    f = L.rq_norm_residual
+    for bad in (dict(dtype=2), dict(post=3), dict(post=-1), dict(pre=3), dict(act=3), dict(act=-1), dict(ep=-1.0),
+                dict(e=float("nan"))):
+        assert f(*norm_args(**bad)) == rq.ERR_RANGE, bad
+    for bad in (dict(M=0), dict(D=0), dict(D=100), dict(D=16448, ldy=1 << 20), dict(group=4), dict(group=48),
+                dict(group=512), dict(group=256), dict(ldy=120), dict(ldy=132), dict(lda=64), dict(ldg=129)):
+        assert f(*norm_args(**bad)) == rq.ERR_SHAPE, bad
+    assert f(*norm_args(y=None)) == rq.ERR_NULL
+    assert f(*norm_args(ho=None, x=None)) == rq.ERR_NULL
+    for n in ("y", "pw", "pb", "add", "gate", "h", "alpha", "w", "b", "ho", "x"):
+        assert f(*norm_args(**{n: FAKE + 8})) == rq.ERR_ALIGN, n
+
+
+def test_norm_binding_refuses(L):
+    y = torch.zeros(4, 128)
+    refused(rq.ERR_RANGE, rq.norm_residual, y.double())
+    refused(rq.ERR_RANGE, rq.norm_residual, y, post="batch")
+    refused(rq.ERR_RANGE, rq.norm_residual, y, gate=y, gate_act="relu")
+    refused(rq.ERR_SHAPE, rq.norm_residual, y[0])
+    refused(rq.ERR_SHAPE, rq.norm_residual, torch.zeros(128, 4).T)
+    refused(rq.ERR_SHAPE, rq.norm_residual, y, gate=y.half())
+    refused(rq.ERR_SHAPE, rq.norm_residual, y, add=y[:3])
+    refused(rq.ERR_SHAPE, rq.norm_residual, y, h=torch.zeros(4, 256)[:, :128])
+    refused(rq.ERR_SHAPE, rq.norm_residual, y, alpha=torch.zeros(64))
+    refused(rq.ERR_SHAPE, rq.norm_residual, y, pre="rms", pre_weight=torch.zeros(128).half())
+    refused(rq.ERR_SHAPE, rq.norm_residual, y, x=torch.zeros(4, 128))
+    refused(rq.ERR_SHAPE, rq.norm_residual, y)                   # on the host

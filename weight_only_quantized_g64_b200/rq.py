@@ -81,6 +81,14 @@ def lib():
     L.rq_gemv_p8_g16.restype = i32
     L.rq_gemv_p4a_g32.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp]
     L.rq_gemv_p4a_g32.restype = i32
+    L.rq_lora_work_bytes.argtypes = [i64, i64, i64]
+    L.rq_lora_work_bytes.restype = ctypes.c_size_t
+    L.rq_lora_add.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, i64, i32, i32, vp, vp, vp]
+    L.rq_lora_add.restype = i32
+    f32 = ctypes.c_float
+    L.rq_norm_residual.argtypes = [vp, i64, i64, i64, i32, i32, i64, vp, vp, f32, vp, i64, vp, i64, i32, vp, vp, i32,
+                                   vp, vp, f32, vp, vp, vp]
+    L.rq_norm_residual.restype = i32
     L.rq_tmix_ckpt_bytes.argtypes = [i64, i64, i64]
     L.rq_tmix_ckpt_bytes.restype = ctypes.c_size_t
     L.rq_tmix_scan.argtypes = [vp] * 6 + [i64, i64, i64, i32, vp, i64, vp, vp, vp, i64, vp, vp, vp, vp]
@@ -334,12 +342,13 @@ def _placed(fn):
     """The call runs, and allocates, on its first tensor's device and on the
     given stream (default: that device's current one)."""
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else next(iter(kw.values()), None)
         if not isinstance(first, torch.Tensor) or not first.is_cuda or (
                 stream is None and first.device.index == torch.cuda.current_device()):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
         with torch.cuda.device(first.device), torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 
@@ -363,6 +372,79 @@ def _on_gpu(call: str, t):
 
 
 _REAL = {torch.float32: OUT_F32, torch.float16: OUT_F16}
+
+
+@_placed
+def lora_add(x, A, B, ids, y, out=None, ranks=None, scale=None, epilogue: int = EPI_NONE, dev_status=None):
+    """y [M, N] (fp32 or fp16) plus the low-rank adapters of its tokens: x fp16
+    [M, K], A fp16 [L, R, K], B fp16 [L, N, R], ids int32 [M] (negative: none),
+    ranks int32 [L], scale fp32 [L].  out may be y."""
+    c = "rq_lora_add"
+    _need(x.dim() == 2 and A.dim() == 3 and B.dim() == 3, f"{c}: x [M, K], A [L, R, K] and B [L, N, R] are needed")
+    (M, K), (L, R), N = x.shape, A.shape[:2], B.shape[1]
+    _need(y.dtype in _REAL, f"{c}: y must be float32 or float16, not {y.dtype}", ERR_RANGE)
+    _tensor(c, "x", x, torch.float16, (M, K))
+    _tensor(c, "A", A, torch.float16, (L, R, K), x)
+    _tensor(c, "B", B, torch.float16, (L, N, R), x)
+    _tensor(c, "ids", ids, torch.int32, (M,), x)
+    _tensor(c, "y", y, y.dtype, (M, N), x)
+    for name, t, dtype, shape in (("out", out, y.dtype, (M, N)), ("ranks", ranks, torch.int32, (L,)),
+                                  ("scale", scale, torch.float32, (L,)), ("dev_status", dev_status, torch.int32, (1,))):
+        if t is not None:
+            _tensor(c, name, t, dtype, shape, x)
+    _on_gpu(c, x)
+    if out is None:
+        out = torch.empty_like(y)
+    n = 0 if M <= MAX_DECODE_M else int(lib().rq_lora_work_bytes(M, K, R))
+    work = torch.empty(n // 4, dtype=torch.float32, device=x.device) if n else None
+    _check(lib().rq_lora_add(_p(x), M, K, _p(A), _p(B), L, R, _p(ids), _p(ranks), _p(scale), _p(y), _p(out), N,
+                             _REAL[y.dtype], epilogue, _p(work), _p(dev_status), _stream()), c)
+    return out
+
+
+NORMS = {"none": 0, "layer": 1, "rms": 2}
+GATES = {"identity": 0, "sigmoid": 1, "silu": 2}
+
+
+@_placed
+def norm_residual(y, post: str = "none", post_group: int = 0, post_weight=None, post_bias=None, eps_post: float = 1e-5,
+                  add=None, gate=None, gate_act: str = "identity", h=None, alpha=None, pre: str = "none",
+                  pre_weight=None, pre_bias=None, eps_pre: float = 1e-5, h_out=None, x=None):
+    """One pass between two projections: u = (Norm_post(y) + add) * act(gate),
+    h' = h + alpha u, x = Norm_pre(h') in fp16.  y, add, gate [M, D] fp32 or fp16
+    (rows may be columns of a wider matrix), h [M, D]; weights, biases and alpha
+    fp32 [D].  Returns (h', x); h' is None without h and h_out.  h_out may be h."""
+    c = "rq_norm_residual"
+    _need(y.dim() == 2, f"{c}: y must be [M, D], not {tuple(y.shape)}")
+    _need(y.dtype in _REAL, f"{c}: y must be float32 or float16, not {y.dtype}", ERR_RANGE)
+    _need(post in NORMS and pre in NORMS and gate_act in GATES, f"{c}: {post}, {pre} or {gate_act} is not known",
+          ERR_RANGE)
+    M, D = y.shape
+    ld = [D, D, D]
+    for i, (name, t) in enumerate((("y", y), ("add", add), ("gate", gate))):
+        if t is not None:
+            if t.dtype != y.dtype or t.shape != y.shape or t.stride(1) != 1 or t.device != y.device:
+                raise RQError(ERR_SHAPE, f"{c}: {name} must be {y.dtype} {(M, D)} on {y.device} with rows of stride 1, "
+                                         f"not {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
+            if M > 1:
+                ld[i] = t.stride(0)
+    for name, t, dtype, shape in (("h", h, y.dtype, (M, D)), ("h_out", h_out, y.dtype, (M, D)),
+                                  ("x", x, torch.float16, (M, D)), ("post_weight", post_weight, torch.float32, (D,)),
+                                  ("post_bias", post_bias, torch.float32, (D,)), ("alpha", alpha, torch.float32, (D,)),
+                                  ("pre_weight", pre_weight, torch.float32, (D,)),
+                                  ("pre_bias", pre_bias, torch.float32, (D,))):
+        if t is not None:
+            _tensor(c, name, t, dtype, shape, y)
+    _on_gpu(c, y)
+    if h_out is None and h is not None:
+        h_out = torch.empty_like(h)
+    if x is None:
+        x = torch.empty((M, D), dtype=torch.float16, device=y.device)
+    _check(lib().rq_norm_residual(_p(y), ld[0], M, D, _REAL[y.dtype], NORMS[post], post_group, _p(post_weight),
+                                  _p(post_bias), eps_post, _p(add), ld[1], _p(gate), ld[2], GATES[gate_act], _p(h),
+                                  _p(alpha), NORMS[pre], _p(pre_weight), _p(pre_bias), eps_pre, _p(h_out), _p(x),
+                                  _stream()), c)
+    return h_out, x
 
 
 def _heads(call: str, names: str, tensors):
