@@ -1,18 +1,20 @@
 // rq_lora.cu -- low-rank adapters of many requests beside one product:
 //   out[m] = epi(y[m] + s_a B_a (A_a x[m])),   a = ids[m].
 //
-// Few tokens (decode): a cluster of 8 CTAs per token, one launch.  Each CTA
-// forms A x over an eighth of K, sends its R sums to all eight, and after one
-// cluster barrier adds them in rank order and takes an eighth of the outputs;
-// its first rows of B are already on their way then.  Bound by latency: two
-// dependent reads of memory and a barrier.
+// One launch either way: a cluster of CTAs splits K for A x, exchanges the R
+// sums of each token through distributed shared memory, and splits N for B.
 //
-// Many tokens (prefill): tiles of 64 tokens on the warp-level tensor cores,
-// two launches (A x split over K into the workspace, then B).  The products of
-// the first are exact in fp32; the second splits each fp32 sum t into two fp16
-// parts, t = 2^-e (hi + lo) with |t| 2^e scaled near 2^14 per token, so 22 bits
-// of t enter the product.  Bound by the bytes of x, y and out.  A tile whose
-// tokens use several adapters takes them in turn and keeps each token's own.
+// Few tokens (decode): a cluster of 8 per token, plain fp32 sums.  Its part of
+// B (one contiguous piece) is sent for into L2 at the start, and its first rows
+// into registers before the cluster meets.  Bound by latency: two dependent
+// reads of memory and a barrier.
+//
+// Many tokens (prefill): a cluster per 64 tokens on the warp-level tensor
+// cores.  The products of A x are exact in fp32; for B each fp32 sum t is split
+// into two fp16 parts, t = 2^-e (hi + lo), scaled per token so that the largest
+// lies near 2^14, so 22 bits of it enter the product.  Bound by the bytes of x,
+// y and out.  A tile whose tokens use several adapters takes them in turn and
+// keeps each token's own.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -20,6 +22,7 @@
 #include <climits>
 
 #include "rq_lora.h"
+#include "rq_once.h"
 #include "rq_ptx.cuh"
 
 namespace rq {
@@ -84,6 +87,11 @@ __global__ void __launch_bounds__(TT) lora_token_kernel(const LoraArgs p) {
         return;
     }
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    if (threadIdx.x == 0 && n1 > n0) {
+        const char* from = reinterpret_cast<const char*>(p.B + (static_cast<int64_t>(a) * p.N + n0) * p.R);
+        const uint32_t size = static_cast<uint32_t>(min((n1 - n0) * p.R * 2, int64_t{1} << 20));
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(size) : "memory");
+    }
 
     // A x over this CTA's part of K; warp w takes ranks w, w + 8, ...
     const int rank = rank_of(p, a);
@@ -208,6 +216,7 @@ constexpr int TM = 64;                       // tokens of a tile
 constexpr int KT = 64;                       // k of a stage
 constexpr int NT = 128;                      // outputs of a tile
 constexpr int LDK = KT + 8;                  // halves; 16-byte pieces of 8 rows meet no bank twice
+constexpr int STAGES = 3;
 
 __device__ __forceinline__ void cp16(void* dst, const void* src, bool live) {
     const int n = live ? 16 : 0;             // 0: the destination is filled with zeros
@@ -244,42 +253,97 @@ __device__ __forceinline__ int next_adapter(const int* ids, int after) {
     return __reduce_min_sync(0xffffffffu, best);
 }
 
-// t[split][m][r] = sum over the split's k of x[m, k] A[r, k]
-template <int RT>                            // tiles of 8 ranks (R <= 8 RT)
-__global__ void __launch_bounds__(128) lora_shrink_kernel(const LoraArgs p) {
-    constexpr int STAGES = 3;
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    __half (*xs)[TM][LDK] = reinterpret_cast<__half (*)[TM][LDK]>(smem_raw);
-    __half (*as)[RT * 8][LDK] = reinterpret_cast<__half (*)[RT * 8][LDK]>(smem_raw + sizeof(__half) * STAGES * TM * LDK);
-    __shared__ int ids[TM];
-    const int m0 = blockIdx.x * TM, split = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < TM) ids[threadIdx.x] = m0 + threadIdx.x < p.M ? adapter_of(p, m0 + threadIdx.x) : -1;
-    __syncthreads();
-    const int steps = (p.K + KT - 1) / KT;
-    const int s0 = static_cast<int64_t>(steps) * split / p.ksplit, s1 = static_cast<int64_t>(steps) * (split + 1) / p.ksplit;
-    const __half* X = reinterpret_cast<const __half*>(p.x);
-    const __half* Ab = reinterpret_cast<const __half*>(p.A);
+// Four consecutive outputs of row m from column n on; `wide`: 4 | N.
+template <typename T>
+__device__ __forceinline__ void get4(const void* p, int64_t at, int64_t left, bool wide, float f[4]) {
+    if (wide && left >= 4) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+            f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __half*>(p) + at);
+            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+            f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = j < left ? get<T>(p, at + j) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void put4(void* p, int64_t at, int64_t left, bool wide, const float f[4]) {
+    if (wide && left >= 4) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+            const __half2 a = __floats2half2_rn(f[0], f[1]), b = __floats2half2_rn(f[2], f[3]);
+            *reinterpret_cast<uint2*>(static_cast<__half*>(p) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < left) put<T>(p, at + j, f[j]);
+}
 
-    for (int a = next_adapter(ids, -1); a != INT_MAX; a = next_adapter(ids, a)) {
-        const __half* A = Ab + static_cast<int64_t>(a) * p.R * p.K;
+// RT: tiles of 8 ranks (R <= 8 RT)
+template <int RT>
+struct TileSmem {
+    static constexpr int RK = RT < 2 ? 1 : RT / 2;       // steps of 16 ranks
+    static constexpr int LDR = RK * 16 + 8;
+    static constexpr int LDP = RT * 8 + 4;
+    union {
+        struct {
+            __half x[STAGES][TM][LDK], a[STAGES][RT * 8][LDK];
+        } in;
+        __half b[2][NT][LDR];
+    };
+    __half hi[TM][LDR], lo[TM][LDR];
+    float part[TM][LDP];
+    float back[TM];                          // 2^-e of each token
+    int ids[TM];
+};
+
+template <typename T, int RT>
+__global__ void __launch_bounds__(256, RT <= 8 ? 2 : 1) lora_tile_kernel(const LoraArgs p) {
+    using Smem = TileSmem<RT>;
+    constexpr int RK = Smem::RK;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = cluster.num_blocks(), me = cluster.block_rank();
+    const int m0 = blockIdx.x / ctas * TM;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    if (tid < TM) sm.ids[tid] = m0 + tid < p.M ? adapter_of(p, m0 + tid) : -1;
+    __syncthreads();
+
+    // ---- part[m][r] = sum over this CTA's k of x[m, k] A[r, k]; a warp takes 16 tokens and half of each stage
+    const int steps = (p.K + KT - 1) / KT;
+    const int s0 = static_cast<int64_t>(steps) * me / ctas, s1 = static_cast<int64_t>(steps) * (me + 1) / ctas;
+    const int mw = (warp & 3) * 16, kh = warp >> 2, g = lane >> 2, q = lane & 3;
+    const __half* X = reinterpret_cast<const __half*>(p.x);
+    for (int a = next_adapter(sm.ids, -1); a != INT_MAX; a = next_adapter(sm.ids, a)) {
+        const __half* A = reinterpret_cast<const __half*>(p.A) + static_cast<int64_t>(a) * p.R * p.K;
         const auto stage = [&](int step) {
             if (step < s1) {
-                const int k0 = step * KT, b = step % STAGES;
-                for (int i = threadIdx.x; i < TM * (KT / 8); i += 128) {
+                const int k0 = step * KT, b = (step - s0) % STAGES;
+#pragma unroll
+                for (int i = tid; i < TM * (KT / 8); i += 256) {
                     const int r = i >> 3, c = (i & 7) * 8;
                     const bool live = m0 + r < p.M && k0 + c < p.K;
-                    cp16(&xs[b][r][c], live ? X + static_cast<int64_t>(m0 + r) * p.K + k0 + c : X, live);
+                    cp16(&sm.in.x[b][r][c], live ? X + static_cast<int64_t>(m0 + r) * p.K + k0 + c : X, live);
                 }
-                for (int i = threadIdx.x; i < RT * 8 * (KT / 8); i += 128) {
+                for (int i = tid; i < RT * 8 * (KT / 8); i += 256) {
                     const int r = i >> 3, c = (i & 7) * 8;
                     const bool live = r < p.R && k0 + c < p.K;
-                    cp16(&as[b][r][c], live ? A + static_cast<int64_t>(r) * p.K + k0 + c : A, live);
+                    cp16(&sm.in.a[b][r][c], live ? A + static_cast<int64_t>(r) * p.K + k0 + c : A, live);
                 }
             }
             cp_commit();
         };
-        const bool mine = __any_sync(0xffffffffu, ids[warp * 16 + (lane & 15)] == a);
+        const bool mine = __any_sync(0xffffffffu, sm.ids[mw + (lane & 15)] == a);
         float acc[RT][4];
 #pragma unroll
         for (int n = 0; n < RT; ++n)
@@ -291,197 +355,207 @@ __global__ void __launch_bounds__(128) lora_shrink_kernel(const LoraArgs p) {
             cp_wait<STAGES - 2>();
             __syncthreads();
             stage(step + STAGES - 1);
-            const int b = step % STAGES;
+            const int b = (step - s0) % STAGES;
             if (mine) {
 #pragma unroll
-                for (int k = 0; k < KT; k += 16) {
+                for (int k = kh * 32; k < kh * 32 + 32; k += 16) {
                     uint32_t fx[4];
-                    ldsm4(fx, &xs[b][warp * 16 + (lane & 15)][k + (lane >> 4) * 8]);
+                    ldsm4(fx, &sm.in.x[b][mw + (lane & 15)][k + (lane >> 4) * 8]);
 #pragma unroll
                     for (int n = 0; n < RT; ++n) {
                         uint32_t fa[2];
-                        ldsm2(fa, &as[b][n * 8 + (lane & 7)][k + ((lane >> 3) & 1) * 8]);
+                        ldsm2(fa, &sm.in.a[b][n * 8 + (lane & 7)][k + ((lane >> 3) & 1) * 8]);
                         mma(acc[n], fx, fa);
                     }
                 }
             }
         }
         cp_wait<0>();
-        __syncthreads();                     // the stages are free for the next adapter
-        if (!mine) continue;
+        // the two halves of the stages are added through shared memory: part is the second's, then the sum
+        const bool own[2] = {sm.ids[mw + g] == a, sm.ids[mw + g + 8] == a};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = warp * 16 + half * 8 + (lane >> 2);
-            if (ids[r] != a) continue;
-            float* t = p.work + (static_cast<int64_t>(split) * p.M + m0 + r) * p.R + 2 * (lane & 3);
+        for (int turn = 1; turn >= 0; --turn) {
+            if (kh == turn && mine) {
 #pragma unroll
-            for (int n = 0; n < RT; ++n)
-                if (n * 8 < p.R) *reinterpret_cast<float2*>(t + n * 8) = make_float2(acc[n][2 * half], acc[n][2 * half + 1]);
+                for (int half = 0; half < 2; ++half) {
+                    if (!own[half]) continue;
+#pragma unroll
+                    for (int n = 0; n < RT; ++n) {
+                        float2* at = reinterpret_cast<float2*>(&sm.part[mw + g + 8 * half][n * 8 + 2 * q]);
+                        float2 v = make_float2(acc[n][2 * half], acc[n][2 * half + 1]);
+                        if (turn == 0) {
+                            const float2 o = *at;
+                            v = make_float2(v.x + o.x, v.y + o.y);
+                        }
+                        *at = v;
+                    }
+                }
+            }
+            __syncthreads();                 // and the stages are free for the next adapter
         }
     }
-}
 
-// out = epi(y + scale t B^T)
-template <typename T, int RK>                // steps of 16 ranks (R <= 16 RK)
-__global__ void __launch_bounds__(256) lora_expand_kernel(const LoraArgs p) {
-    constexpr int LDR = RK * 16 + 8;
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    __half (*hi)[LDR] = reinterpret_cast<__half (*)[LDR]>(smem_raw);
-    __half (*lo)[LDR] = hi + TM;
-    __half (*bs)[LDR] = lo + TM;
-    __shared__ int ids[TM];
-    __shared__ float back[TM];               // 2^-e of each token
-    const int m0 = blockIdx.y * TM;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * NT;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < TM) ids[threadIdx.x] = m0 + threadIdx.x < p.M ? adapter_of(p, m0 + threadIdx.x) : -1;
-    __syncthreads();
-
-    // this thread's outputs: rows mw + g and mw + g + 8, columns nw + 8 i + 2 q + 0..1
-    const int mw = (warp & 3) * 16, g = lane >> 2, q = lane & 3;
-    const int64_t nw = n0 + (warp >> 2) * 64;
-    const bool pairs = (p.N & 1) == 0;
-    float acc[8][4], yv[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int m = m0 + mw + g + 8 * half;
-            const int64_t n = nw + 8 * i + 2 * q, at = static_cast<int64_t>(m) * p.N + n;
-            acc[i][2 * half] = acc[i][2 * half + 1] = 0.f;
-            yv[i][2 * half] = yv[i][2 * half + 1] = 0.f;
-            if (m >= p.M || n >= p.N) continue;
-            if (pairs) {
-                float2 f;
-                if constexpr (sizeof(T) == 4) f = *reinterpret_cast<const float2*>(static_cast<const float*>(p.y) + at);
-                else f = __half22float2(*reinterpret_cast<const __half2*>(static_cast<const __half*>(p.y) + at));
-                yv[i][2 * half] = f.x;
-                yv[i][2 * half + 1] = f.y;
-            } else {
-                yv[i][2 * half] = get<T>(p.y, at);
-                if (n + 1 < p.N) yv[i][2 * half + 1] = get<T>(p.y, at + 1);
-            }
+    // ---- B of the first tile on its way, then the cluster's sums
+    const int tiles = static_cast<int>((p.N + NT - 1) / NT);
+    const auto fetch = [&](int tile, int a, int buf) {
+        const int rank = rank_of(p, a);
+        const __half* B = reinterpret_cast<const __half*>(p.B) + static_cast<int64_t>(a) * p.N * p.R;
+        const int64_t n0 = static_cast<int64_t>(tile) * NT;
+#pragma unroll 4
+        for (int i = tid; i < NT * RK * 2; i += 256) {
+            const int r = i / (RK * 2), c = (i % (RK * 2)) * 8;
+            const bool live = n0 + r < p.N && c < rank;
+            cp16(&sm.b[buf][r][c], live ? B + (n0 + r) * p.R + c : B, live);
         }
-
-    // t of each token, in two fp16 parts; four threads a token
-    {
-        const int r = threadIdx.x >> 2, c0 = threadIdx.x & 3, a = ids[r];
+        cp_commit();
+    };
+    const int first = next_adapter(sm.ids, -1);
+    if (first != INT_MAX && me < tiles) fetch(me, first, 0);
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    {                                        // four threads a token
+        const int r = tid >> 2, c0 = (tid & 3) * 4, a = sm.ids[r];
         const int rank = a >= 0 ? rank_of(p, a) : 0;
         const float s = a >= 0 && p.scale != nullptr ? p.scale[a] : 1.f;
-        float t[RK * 4], top = 0.f;
+        float t[RK][4], top = 0.f;
 #pragma unroll
-        for (int i = 0; i < RK * 4; ++i) {
-            const int c = c0 + 4 * i;
-            float f = 0.f;
-            if (c < rank)
-                for (int k = 0; k < p.ksplit; ++k) f += p.work[(static_cast<int64_t>(k) * p.M + m0 + r) * p.R + c];
-            t[i] = c < rank ? f * s : 0.f;
-            const float mag = fabsf(t[i]);
-            top = mag <= FLT_MAX ? fmaxf(top, mag) : top;    // infinities and NaN pass as they are
+        for (int i = 0; i < RK; ++i) {
+            const int c = c0 + 16 * i;
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < rank) {
+                for (int k = 0; k < ctas; ++k) {
+                    const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&sm.part[r][c], k));
+                    f.x += v.x; f.y += v.y; f.z += v.z; f.w += v.w;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                t[i][j] = c + j < rank ? (&f.x)[j] * s : 0.f;
+                const float mag = fabsf(t[i][j]);
+                top = mag <= FLT_MAX ? fmaxf(top, mag) : top;    // infinities and NaN pass as they are
+            }
         }
+        // no CTA leaves before the others have read its sums
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // the power of two that brings the largest |t| into [2^14, 2^15)
         const int ex = static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127;
         const int e = top > 0.f ? min(14 - ex, 100) : 0;
         const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        if (c0 == 0) back[r] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        if ((tid & 3) == 0) sm.back[r] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-        for (int i = 0; i < RK * 4; ++i) {
-            const float f = t[i] * up;
-            const __half h = __float2half_rn(f);
-            const float rest = f - __half2float(h);
-            hi[r][c0 + 4 * i] = h;
-            lo[r][c0 + 4 * i] = __float2half_rn(fabsf(f) <= 65504.f ? rest : 0.f);   // an infinite t has no rest
-        }
-    }
-
-    for (int a = next_adapter(ids, -1); a != INT_MAX; a = next_adapter(ids, a)) {
-        const int rank = rank_of(p, a);
-        const __half* B = reinterpret_cast<const __half*>(p.B) + static_cast<int64_t>(a) * p.N * p.R;
-        for (int i = threadIdx.x; i < NT * RK * 2; i += 256) {
-            const int r = i / (RK * 2), c = (i % (RK * 2)) * 8;
-            const bool live = n0 + r < p.N && c < rank;
-            cp16(&bs[r][c], live ? B + (n0 + r) * p.R + c : B, live);
-        }
-        cp_commit();
-        cp_wait<0>();
-        __syncthreads();
-        if (rank & 7) {                      // columns behind the rank share its last piece: not the adapter's
-            const int c = rank + threadIdx.x / NT;
-            for (int cc = c; cc < (rank | 7) + 1; cc += 2) bs[threadIdx.x % NT][cc] = __float2half_rn(0.f);
-            __syncthreads();
-        }
-        if (__any_sync(0xffffffffu, ids[mw + (lane & 15)] == a)) {
-            const bool own0 = ids[mw + g] == a, own1 = ids[mw + g + 8] == a;
-            uint32_t fh[RK][4], fl[RK][4];
+        for (int i = 0; i < RK; ++i)
 #pragma unroll
-            for (int k = 0; k < RK; ++k) {
-                ldsm4(fh[k], &hi[mw + (lane & 15)][k * 16 + (lane >> 4) * 8]);
-                ldsm4(fl[k], &lo[mw + (lane & 15)][k * 16 + (lane >> 4) * 8]);
+            for (int j = 0; j < 4; ++j) {
+                const float f = t[i][j] * up;
+                const __half h = __float2half_rn(f);
+                sm.hi[r][c0 + 16 * i + j] = h;
+                // an infinite t has no rest
+                sm.lo[r][c0 + 16 * i + j] = __float2half_rn(fabsf(f) <= 65504.f ? f - __half2float(h) : 0.f);
             }
+    }
+    __syncthreads();
+
+    // ---- out = epi(y + t B^T); warp: 16 tokens x 64 outputs of a tile.  A thread's columns of a pair of 8-column
+    // products are four neighbours: product column c of product i stands for output 16 (i / 2) + 4 (c / 2) + 2 (i % 2)
+    // + c % 2.
+    const bool wide = (p.N & 3) == 0;
+    const int64_t rows[2] = {m0 + mw + g, m0 + mw + g + 8};
+    const float back[2] = {sm.ids[mw + g] >= 0 ? sm.back[mw + g] : 0.f,
+                           sm.ids[mw + g + 8] >= 0 ? sm.back[mw + g + 8] : 0.f};
+    int buf = 0;
+    for (int tile = me; tile < tiles; tile += ctas) {
+        const int64_t nw = static_cast<int64_t>(tile) * NT + (warp >> 2) * 64 + 4 * q;
+        float acc[4][2][4];                  // [16 outputs][row half][neighbour]: y, then the sum
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                if (rows[half] < p.M)
+                    get4<T>(p.y, rows[half] * p.N + nw + 16 * i, p.N - nw - 16 * i, wide, acc[i][half]);
+        for (int a = first; a != INT_MAX;) {
+            const int after = next_adapter(sm.ids, a);
+            if (after != INT_MAX) fetch(tile, after, buf ^ 1);
+            else if (tile + ctas < tiles) fetch(tile + ctas, first, buf ^ 1);
+            else cp_commit();
+            cp_wait<1>();
+            __syncthreads();
+            const int rank = rank_of(p, a);
+            if (rank & 7) {                  // columns behind the rank share its last piece: not the adapter's
+                for (int c = rank + tid / NT; c < (rank | 7) + 1; c += 2) sm.b[buf][tid % NT][c] = __float2half_rn(0.f);
+                __syncthreads();
+            }
+            if (__any_sync(0xffffffffu, sm.ids[mw + (lane & 15)] == a)) {
+                float c[8][4];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
 #pragma unroll
                 for (int k = 0; k < RK; ++k) {
-                    uint32_t fb[2];
-                    ldsm2(fb, &bs[(warp >> 2) * 64 + i * 8 + (lane & 7)][k * 16 + ((lane >> 3) & 1) * 8]);
-                    mma(c, fl[k], fb);
-                    mma(c, fh[k], fb);
+                    uint32_t fh[4], fl[4];
+                    ldsm4(fh, &sm.hi[mw + (lane & 15)][k * 16 + (lane >> 4) * 8]);
+                    ldsm4(fl, &sm.lo[mw + (lane & 15)][k * 16 + (lane >> 4) * 8]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int col = lane & 7;
+                        uint32_t fb[2];
+                        ldsm2(fb, &sm.b[buf][(warp >> 2) * 64 + 16 * (i >> 1) + 4 * (col >> 1) + 2 * (i & 1) + (col & 1)]
+                                        [k * 16 + ((lane >> 3) & 1) * 8]);
+                        mma(c[i], fl, fb);
+                        mma(c[i], fh, fb);
+                    }
                 }
-                acc[i][0] = own0 ? c[0] : acc[i][0];
-                acc[i][1] = own0 ? c[1] : acc[i][1];
-                acc[i][2] = own1 ? c[2] : acc[i][2];
-                acc[i][3] = own1 ? c[3] : acc[i][3];
-            }
-        }
-        __syncthreads();
-    }
-
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int r = mw + g + 8 * half, m = m0 + r;
-        if (m >= p.M) continue;
-        const bool has = ids[r] >= 0;
-        const float b = has ? back[r] : 0.f;
+                for (int half = 0; half < 2; ++half) {
+                    if (sm.ids[mw + g + 8 * half] != a) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t n = nw + 8 * i + 2 * q, at = static_cast<int64_t>(m) * p.N + n;
-            if (n >= p.N) continue;
-            float f0 = yv[i][2 * half], f1 = yv[i][2 * half + 1];
-            if (has) {
-                f0 = fmaf(acc[i][2 * half], b, f0);
-                f1 = fmaf(acc[i][2 * half + 1], b, f1);
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float& f = acc[i >> 1][half][2 * (i & 1) + j];
+                            f = fmaf(c[i][2 * half + j], back[half], f);
+                        }
+                }
             }
-            f0 = finish(f0, p.relu_sq);
-            f1 = finish(f1, p.relu_sq);
-            if (pairs) {
-                if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(f0, f1);
-                else *reinterpret_cast<__half2*>(static_cast<__half*>(p.out) + at) = __floats2half2_rn(f0, f1);
-            } else {
-                put<T>(p.out, at, f0);
-                if (n + 1 < p.N) put<T>(p.out, at + 1, f1);
-            }
+            __syncthreads();
+            buf ^= 1;
+            a = after;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (rows[half] >= p.M) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][half][j] = finish(acc[i][half][j], p.relu_sq);
+                put4<T>(p.out, rows[half] * p.N + nw + 16 * i, p.N - nw - 16 * i, wide, acc[i][half]);
+            }
     }
+    cp_wait<0>();
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-template <int RT>
-cudaError_t launch_shrink(const LoraArgs& a, cudaStream_t s) {
-    constexpr int smem = 3 * (TM + RT * 8) * LDK * 2;
-    const cudaError_t e = cudaFuncSetAttribute(lora_shrink_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename T, int RT>
+cudaError_t launch_tiles(const LoraArgs& a, cudaStream_t s) {
+    constexpr int smem = sizeof(TileSmem<RT>);
+    cudaError_t e = allow_smem<lora_tile_kernel<T, RT>>(smem);
     if (e != cudaSuccess) return e;
-    lora_shrink_kernel<RT><<<dim3((a.M + TM - 1) / TM, a.ksplit), 128, smem, s>>>(a);
-    return cudaGetLastError();
-}
-template <typename T, int RK>
-cudaError_t launch_expand(const LoraArgs& a, cudaStream_t s) {
-    constexpr int smem = (2 * TM + NT) * (RK * 16 + 8) * 2;
-    const cudaError_t e = cudaFuncSetAttribute(lora_expand_kernel<T, RK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    lora_expand_kernel<T, RK><<<dim3(static_cast<unsigned>((a.N + NT - 1) / NT), (a.M + TM - 1) / TM), 256, smem, s>>>(a);
-    return cudaGetLastError();
+    const int tiles = (a.M + TM - 1) / TM;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * CS);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lora_tile_kernel<T, RT>, a);
 }
 
 template <typename T>
@@ -494,36 +568,23 @@ cudaError_t tokens(const LoraArgs& a, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t tiles(const LoraArgs& a, cudaStream_t s) {
-    const cudaError_t e = a.R <= 8    ? launch_shrink<1>(a, s)
-                          : a.R <= 16 ? launch_shrink<2>(a, s)
-                          : a.R <= 32 ? launch_shrink<4>(a, s)
-                          : a.R <= 64 ? launch_shrink<8>(a, s)
-                                      : launch_shrink<16>(a, s);
-    if (e != cudaSuccess) return e;
-    return a.R <= 16   ? launch_expand<T, 1>(a, s)
-           : a.R <= 32 ? launch_expand<T, 2>(a, s)
-           : a.R <= 64 ? launch_expand<T, 4>(a, s)
-                       : launch_expand<T, 8>(a, s);
+    return a.R <= 8    ? launch_tiles<T, 1>(a, s)
+           : a.R <= 16 ? launch_tiles<T, 2>(a, s)
+           : a.R <= 32 ? launch_tiles<T, 4>(a, s)
+           : a.R <= 64 ? launch_tiles<T, 8>(a, s)
+                       : launch_tiles<T, 16>(a, s);
 }
 
 bool mis(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 rq_status check_sizes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t R) {
-    if (M < 1 || M > 64 * 65535 || K < 8 || K % 8 != 0 || K > (1 << 30)) return RQ_ERR_SHAPE;
+    if (M < 1 || M >= (1 << 24) || K < 8 || K % 8 != 0 || K > (1 << 30)) return RQ_ERR_SHAPE;
     if (N < 1 || N > (int64_t{1} << 31) - 1 || L < 1 || L > (1 << 30)) return RQ_ERR_SHAPE;
     if (R < 8 || R % 8 != 0 || R > RQ_MAX_LORA_RANK) return RQ_ERR_SHAPE;
     return RQ_OK;
 }
 
 }  // namespace
-
-// Enough CTAs for two per SM, each with at least four stages of k.
-int lora_ksplit(int64_t M, int64_t K) {
-    const int64_t tiles = (M + TM - 1) / TM, steps = (K + KT - 1) / KT;
-    int64_t s = (2 * 148 + tiles - 1) / tiles;
-    if (s > steps / 4) s = steps / 4;
-    return static_cast<int>(s < 1 ? 1 : s > 32 ? 32 : s);
-}
 
 cudaError_t launch_lora_tokens(const LoraArgs& a, bool half, cudaStream_t s) {
     return half ? tokens<__half>(a, s) : tokens<float>(a, s);
@@ -538,23 +599,16 @@ using namespace rq;
 
 extern "C" {
 
-size_t rq_lora_work_bytes(int64_t M, int64_t K, int64_t R) {
-    if (check_sizes(M, K, 1, 1, R) != RQ_OK || M <= kLoraTokens) return 0;
-    return static_cast<size_t>(lora_ksplit(M, K)) * M * R * sizeof(float);
-}
-
 rq_status rq_lora_add(const uint16_t* x, int64_t M, int64_t K, const uint16_t* A, const uint16_t* B, int64_t L,
                       int64_t R, const int32_t* ids, const int32_t* ranks, const float* scale, const void* y,
-                      void* out, int64_t N, int dtype, int epilogue, float* work, int* dev_status,
-                      rq_stream_t stream) {
+                      void* out, int64_t N, int dtype, int epilogue, int* dev_status, rq_stream_t stream) {
     if (dtype != RQ_OUT_F32 && dtype != RQ_OUT_F16) return RQ_ERR_RANGE;
     if (epilogue != RQ_EPI_NONE && epilogue != RQ_EPI_RELU_SQ) return RQ_ERR_RANGE;
     const rq_status st = check_sizes(M, K, N, L, R);
     if (st != RQ_OK) return st;
     if (x == nullptr || A == nullptr || B == nullptr || ids == nullptr || y == nullptr || out == nullptr)
         return RQ_ERR_NULL;
-    if (work == nullptr && M > kLoraTokens) return RQ_ERR_NULL;
-    if (mis(x, 16) || mis(A, 16) || mis(B, 16) || mis(y, 16) || mis(out, 16) || mis(work, 16) || mis(ids, 4) ||
+    if (mis(x, 16) || mis(A, 16) || mis(B, 16) || mis(y, 16) || mis(out, 16) || mis(ids, 4) ||
         mis(ranks, 4) || mis(scale, 4) || mis(dev_status, 4))
         return RQ_ERR_ALIGN;
     LoraArgs a = {};
@@ -566,14 +620,12 @@ rq_status rq_lora_add(const uint16_t* x, int64_t M, int64_t K, const uint16_t* A
     a.scale = scale;
     a.y = y;
     a.out = out;
-    a.work = work;
     a.status = dev_status;
     a.N = N;
     a.M = static_cast<int>(M);
     a.K = static_cast<int>(K);
     a.R = static_cast<int>(R);
     a.L = static_cast<int>(L);
-    a.ksplit = lora_ksplit(M, K);
     a.relu_sq = epilogue == RQ_EPI_RELU_SQ;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool half = dtype == RQ_OUT_F16;

@@ -3,16 +3,22 @@
 //
 //   u = (Norm_post(y) + add) * act(gate);   h' = h + alpha u;   x = Norm_pre(h')
 //
-// One CTA per row; a thread holds V pieces of 8 channels in registers, so each
-// tensor is read once and each result written once: bound by those bytes.
+// A CTA takes a row at a time; a thread holds V pieces of 8 channels in
+// registers, so each tensor is read once and each result written once: bound by
+// those bytes.  Rows of up to 4096 channels are taken by CTAs that stay and
+// bring the next rows' pieces into shared memory meanwhile (a thread waits for
+// its own pieces only); longer rows, whose ring would not fit, are loaded as
+// they come, a CTA each.
 // Mean and squared deviation come from one reduction: every thread forms them
 // over its own values (two passes over registers) and pairs are joined by
 //   delta = m2 - m1;  m = m1 + delta n2/(n1+n2);  M2 = M2_1 + M2_2 + delta^2 n1 n2/(n1+n2),
 // which loses nothing when the mean is large against the deviation.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <algorithm>
 
 #include "rq_norm.h"
+#include "rq_once.h"
 
 namespace rq {
 namespace {
@@ -31,15 +37,13 @@ __device__ __forceinline__ Moments join_xor(Moments a, int mask) {
 }
 
 template <typename T>
-__device__ __forceinline__ void load8(const void* base, int64_t at, float* f) {
-    const T* p = static_cast<const T*>(base) + at;
+__device__ __forceinline__ void expand8(uint4 a, uint4 b, float* f) {
     if constexpr (sizeof(T) == 4) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        const float4 x = *reinterpret_cast<const float4*>(&a), y = *reinterpret_cast<const float4*>(&b);
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
     } else {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-        const __half2* h = reinterpret_cast<const __half2*>(&u);
+        const __half2* h = reinterpret_cast<const __half2*>(&a);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 v = __half22float2(h[i]);
@@ -47,6 +51,16 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, float* f) {
             f[2 * i + 1] = v.y;
         }
     }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const void* base, int64_t at, float* f) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at);
+    expand8<T>(__ldg(p), sizeof(T) == 4 ? __ldg(p + 1) : make_uint4(0u, 0u, 0u, 0u), f);
+}
+template <typename T>
+__device__ __forceinline__ void read8(const void* from, float* f) {
+    const uint4* p = static_cast<const uint4*>(from);
+    expand8<T>(p[0], sizeof(T) == 4 ? p[1] : make_uint4(0u, 0u, 0u, 0u), f);
 }
 template <typename T>
 __device__ __forceinline__ void store8(void* base, int64_t at, const float* f) {
@@ -100,108 +114,163 @@ __device__ __forceinline__ void stats(const float (*v)[8], int pieces, bool laye
     rstd = rsqrtf(a.m2 / a.n + eps);
 }
 
-template <int V>
-__device__ __forceinline__ void apply(float (*v)[8], int pieces, const NormArgs& p, bool post, int threads, float mean,
-                                      float rstd) {
+__device__ __forceinline__ void apply(float* v, const NormArgs& p, bool post, int c, float mean, float rstd) {
     const float* w = post ? p.post_weight : p.pre_weight;
     const float* b = post ? p.post_bias : p.pre_bias;
+    float f[8];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (i >= pieces) break;
-        const int c = (threadIdx.x + i * threads) * 8;
-        float wv[8], bv[8];
-        if (w != nullptr) load8<float>(w, c, wv);
-        if (b != nullptr) load8<float>(b, c, bv);
+    for (int j = 0; j < 8; ++j) v[j] = (v[j] - mean) * rstd;
+    if (w != nullptr) {
+        load8<float>(w, c, f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float f = (v[i][j] - mean) * rstd;
-            if (w != nullptr) f *= wv[j];
-            if (b != nullptr) f += bv[j];
-            v[i][j] = f;
+        for (int j = 0; j < 8; ++j) v[j] *= f[j];
+    }
+    if (b != nullptr) {
+        load8<float>(b, c, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += f[j];
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void normed(float (*u)[8], int pieces, const NormArgs& p, bool post, int threads,
+                                       Moments* shared) {
+    const int kind = post ? p.post : p.pre;
+    if (kind == RQ_NORM_NONE) return;
+    const bool layer = kind == RQ_NORM_LAYER;
+    const float eps = post ? p.eps_post : p.eps_pre;
+    float mean, rstd;
+    if (!post || p.post_group == 0) {
+        stats<V>(u, pieces, layer, 0, eps, shared, mean, rstd);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < pieces) apply(u[i], p, post, (threadIdx.x + i * threads) * 8, mean, rstd);
+    } else {                                 // post_group / 8 neighbouring threads hold a group
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            stats<1>(&u[i], i < pieces, layer, p.post_group / 8, eps, nullptr, mean, rstd);
+            if (i < pieces) apply(u[i], p, post, (threadIdx.x + i * threads) * 8, mean, rstd);
         }
     }
 }
 
+// u = (u + add) * act(gate), h' = h + alpha u of the piece at channel c; take(f) gives
+// the next of the tensors that are there.
+template <typename Take>
+__device__ __forceinline__ void combine(float* u, const NormArgs& p, int c, Take&& take) {
+    float f[8];
+    if (p.add != nullptr) {
+        take(f, p.add, p.ld_add);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] += f[j];
+    }
+    if (p.gate != nullptr) {
+        take(f, p.gate, p.ld_gate);
+        const bool silu = p.gate_act == RQ_GATE_SILU;
+        if (p.gate_act != RQ_GATE_IDENTITY) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = __fdividef(silu ? f[j] : 1.f, 1.f + expf(-f[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] *= f[j];
+    }
+    if (p.alpha != nullptr) {
+        load8<float>(p.alpha, c, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] *= f[j];
+    }
+    if (p.h != nullptr) {
+        take(f, p.h, p.D);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] += f[j];
+    }
+}
+
+__device__ __forceinline__ void cp16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+
+// Rows of up to 4096 channels: row blockIdx.x, + gridDim.x, ...; one piece per thread.
+constexpr int RING = 3;                      // rows on their way, the current one among them
+template <typename T>
+__global__ void __launch_bounds__(512, 2) norm_rows_kernel(const NormArgs p) {
+    constexpr int PB = 8 * sizeof(T);        // bytes of a piece
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ Moments shared[2][2][32];     // of alternate rows: one norm alone has one barrier a row
+    const int threads = blockDim.x, tid = threadIdx.x, c = tid * 8;
+    const bool in = c < p.D;
+    const int tensors = 1 + (p.add != nullptr) + (p.gate != nullptr) + (p.h != nullptr);
+    unsigned char* mine = ring + tid * PB;
+    const auto fetch = [&](int64_t row, int slot) {
+        if (row < p.M && in) {
+            unsigned char* to = mine + slot * tensors * threads * PB;
+            const auto one = [&](const void* base, int64_t ld) {
+                const char* from = static_cast<const char*>(base) + (row * ld + c) * static_cast<int64_t>(sizeof(T));
+#pragma unroll
+                for (int i = 0; i < PB; i += 16) cp16(to + i, from + i);
+                to += threads * PB;
+            };
+            one(p.y, p.ld_y);
+            if (p.add != nullptr) one(p.add, p.ld_add);
+            if (p.gate != nullptr) one(p.gate, p.ld_gate);
+            if (p.h != nullptr) one(p.h, p.D);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < RING - 1; ++i) fetch(blockIdx.x + static_cast<int64_t>(i) * gridDim.x, i);
+    int slot = 0, parity = 0;
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+        fetch(row + static_cast<int64_t>(RING - 1) * gridDim.x, slot == 0 ? RING - 1 : slot - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+        float u[1][8];
+        const unsigned char* from = mine + slot * tensors * threads * PB;
+        const auto take = [&](float* f, const void*, int64_t) {
+            read8<T>(from, f);
+            from += threads * PB;
+        };
+        if (in) take(u[0], nullptr, 0);
+        normed<1>(u, in, p, true, threads, shared[parity][0]);
+        if (in) {
+            combine(u[0], p, c, take);
+            if (p.h_out != nullptr) store8<T>(p.h_out, row * p.D + c, u[0]);
+        }
+        if (p.x != nullptr) {
+            normed<1>(u, in, p, false, threads, shared[parity][1]);
+            if (in) store8<__half>(p.x, row * p.D + c, u[0]);
+        }
+        slot = slot == RING - 1 ? 0 : slot + 1;
+        parity ^= 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Longer rows: a CTA each, V pieces per thread.
 template <typename T, int V>
-__global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_residual_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(1024) norm_row_kernel(const NormArgs p) {
     __shared__ Moments shared[2][32];
     const int64_t row = blockIdx.x;
     const int threads = blockDim.x, all = p.D / 8;
-    // pieces threadIdx.x + i * threads < D / 8
-    int pieces = 0;
+    int pieces = 0;                          // threadIdx.x + i * threads < D / 8
 #pragma unroll
     for (int i = 0; i < V; ++i) pieces += static_cast<int>(threadIdx.x) + i * threads < all;
     float u[V][8];
-    // one piece per thread: everything is in flight at once; with more, the
-    // other rows of the SM hide the second group of loads (registers would not
-    // hold it)
-    constexpr bool EARLY = V == 1;
-    float a[8], g[8], h[8];
-    const auto others = [&](int c) {
-        if (p.add != nullptr) load8<T>(p.add, row * p.ld_add + c, a);
-        if (p.gate != nullptr) load8<T>(p.gate, row * p.ld_gate + c, g);
-        if (p.h != nullptr) load8<T>(p.h, row * p.D + c, h);
-    };
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = (threadIdx.x + i * threads) * 8;
-        if (i < pieces) load8<T>(p.y, row * p.ld_y + c, u[i]);
-    }
-    if (EARLY && pieces > 0) others(threadIdx.x * 8);
-    if (p.post != RQ_NORM_NONE) {
-        float mean, rstd;
-        const bool layer = p.post == RQ_NORM_LAYER;
-        if (p.post_group == 0) {
-            stats<V>(u, pieces, layer, 0, p.eps_post, shared[0], mean, rstd);
-            apply<V>(u, pieces, p, true, threads, mean, rstd);
-        } else {                             // a group is 8 width channels of one piece row
-            const int width = p.post_group / 8;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                stats<1>(&u[i], i < pieces, layer, width, p.eps_post, nullptr, mean, rstd);
-                if (i < pieces) {
-                    const int c = (threadIdx.x + i * threads) * 8;
-                    float wv[8], bv[8];
-                    if (p.post_weight != nullptr) load8<float>(p.post_weight, c, wv);
-                    if (p.post_bias != nullptr) load8<float>(p.post_bias, c, bv);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float f = (u[i][j] - mean) * rstd;
-                        if (p.post_weight != nullptr) f *= wv[j];
-                        if (p.post_bias != nullptr) f += bv[j];
-                        u[i][j] = f;
-                    }
-                }
-            }
-        }
-    }
+    for (int i = 0; i < V; ++i)
+        if (i < pieces) load8<T>(p.y, row * p.ld_y + (threadIdx.x + i * threads) * 8, u[i]);
+    normed<V>(u, pieces, p, true, threads, shared[0]);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (i >= pieces) break;
         const int c = (threadIdx.x + i * threads) * 8;
-        float al[8];
-        if (!EARLY) others(c);
-        if (p.alpha != nullptr) load8<float>(p.alpha, c, al);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float f = u[i][j];
-            if (p.add != nullptr) f += a[j];
-            if (p.gate != nullptr) {
-                const float x = g[j];
-                f *= p.gate_act == RQ_GATE_IDENTITY ? x : (p.gate_act == RQ_GATE_SILU ? x : 1.f) / (1.f + expf(-x));
-            }
-            if (p.alpha != nullptr) f *= al[j];
-            if (p.h != nullptr) f += h[j];
-            u[i][j] = f;
-        }
+        combine(u[i], p, c, [&](float* f, const void* base, int64_t ld) { load8<T>(base, row * ld + c, f); });
         if (p.h_out != nullptr) store8<T>(p.h_out, row * p.D + c, u[i]);
     }
     if (p.x == nullptr) return;
-    if (p.pre != RQ_NORM_NONE) {
-        float mean, rstd;
-        stats<V>(u, pieces, p.pre == RQ_NORM_LAYER, 0, p.eps_pre, shared[1], mean, rstd);
-        apply<V>(u, pieces, p, false, threads, mean, rstd);
-    }
+    normed<V>(u, pieces, p, false, threads, shared[1]);
 #pragma unroll
     for (int i = 0; i < V; ++i)
         if (i < pieces) store8<__half>(p.x, row * p.D + (threadIdx.x + i * threads) * 8, u[i]);
@@ -210,10 +279,19 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_residual_kernel(cons
 template <typename T>
 cudaError_t launch(const NormArgs& a, cudaStream_t s) {
     const int pieces = a.D / 8;
-    const auto threads = [&](int v) { return ((pieces + v - 1) / v + 31) / 32 * 32; };
-    const unsigned rows = static_cast<unsigned>(a.M);
-    if (pieces <= 512) norm_residual_kernel<T, 1><<<rows, threads(1), 0, s>>>(a);
-    else norm_residual_kernel<T, 2><<<rows, threads(2), 0, s>>>(a);
+    if (pieces <= 512) {
+        const int threads = (pieces + 31) / 32 * 32;
+        const int tensors = 1 + (a.add != nullptr) + (a.gate != nullptr) + (a.h != nullptr);
+        const int smem = RING * tensors * threads * 8 * static_cast<int>(sizeof(T));   // at most 192 KB
+        const cudaError_t e = allow_smem<norm_rows_kernel<T>>(RING * 4 * 512 * 8 * static_cast<int>(sizeof(T)));
+        if (e != cudaSuccess) return e;
+        // CTAs that an SM holds: 1024 threads at 64 registers, and their rings
+        const int per_sm = std::max(1, std::min(1024 / threads, (220 << 10) / (smem + 2048)));
+        const int64_t grid = std::min<int64_t>(a.M, static_cast<int64_t>(num_sms()) * per_sm);
+        norm_rows_kernel<T><<<static_cast<unsigned>(grid), threads, smem, s>>>(a);
+        return cudaGetLastError();
+    }
+    norm_row_kernel<T, 2><<<static_cast<unsigned>(a.M), ((pieces + 1) / 2 + 31) / 32 * 32, 0, s>>>(a);
     return cudaGetLastError();
 }
 

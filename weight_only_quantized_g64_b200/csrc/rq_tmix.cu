@@ -5,7 +5,7 @@
 // rows are spread over lanes and stay in registers for the whole sequence:
 // four lanes share a row (16 keys each), a lane holds RPL rows.  Per token a
 // lane reads its 16 keys of five vectors from shared memory once for all its
-// rows; the dot products finish with two shuffles.  Two producer warps load
+// rows; the dot products finish with two shuffles.  Four producer warps load
 // and convert the next chunk of tokens (the decay costs an exponential and a
 // sigmoid per channel) while the others run through the current one.
 // What bounds it: 5 * 64 * 64 fp32 FMA per token and head (packed in pairs),
@@ -21,7 +21,8 @@ namespace rq {
 namespace {
 
 constexpr int CT = kTmixChunk;               // tokens staged at once
-constexpr int NPW = 2;                       // producer warps
+constexpr int NPW = 4;                       // producer warps: one piece of each vector per thread
+static_assert(NPW * 32 == CT * kHead / 8);
 // vectors staged per token: decay - 1, then forward k, a, b, r; backward r, b, a
 constexpr int nvec(bool rev) { return rev ? 4 : 5; }
 
@@ -37,60 +38,54 @@ struct Smem {
 };
 
 // The producers' part of a chunk: tokens [t0, t0 + nt) of head h, from global
-// memory into a stage.
+// memory into registers (one piece of 8 elements of each vector per thread) ...
 template <typename T, int ROWS, bool REV>
-__device__ __forceinline__ void fill(const TmixArgs& p, Stage<ROWS, REV>& st, int64_t t0, int nt, int h,
-                                     int row0, int pt) {
+struct Raw {
+    Raw8 vec[nvec(REV)], row;
+};
+template <typename T, int ROWS, bool REV>
+__device__ __forceinline__ void load_chunk(const TmixArgs& p, Raw<T, ROWS, REV>& raw, int64_t t0, int nt, int h,
+                                           int row0, int pt) {
     // in[]: r, d, k, v, a, b.  Order of the staged vectors (source indices):
     constexpr int src[5] = {1, REV ? 0 : 2, REV ? 5 : 4, REV ? 4 : 5, 0};
-    constexpr int PIECES = CT * (kHead / 8) / (NPW * 32);
-    Raw8 raw[nvec(REV)][PIECES];
+    const int t = pt >> 3, c = (pt & 7) * 8;
+    const int64_t head = static_cast<int64_t>(h) * kHead;
+    if (t < nt) {
 #pragma unroll
-    for (int v = 0; v < nvec(REV); ++v) {
-        const T* base = static_cast<const T*>(p.in[src[v]]) + static_cast<int64_t>(h) * kHead;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            const int piece = pt + i * NPW * 32, t = piece >> 3, c = (piece & 7) * 8;
-            if (t < nt) raw[v][i] = load8(base + (t0 + t) * p.ld + c);
-        }
+        for (int v = 0; v < nvec(REV); ++v)
+            raw.vec[v] = load8(static_cast<const T*>(p.in[src[v]]) + (t0 + t) * p.ld + head + c);
     }
-    constexpr int RP = CT * ROWS / 8, RPT = (RP + NPW * 32 - 1) / (NPW * 32);
-    Raw8 rr[RPT];
-#pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-        const int piece = pt + i * NPW * 32, t = piece / (ROWS / 8), c = (piece % (ROWS / 8)) * 8;
-        if (t < nt) {
-            const T* src_row = REV ? static_cast<const T*>(p.dy) + (t0 + t) * p.H * kHead
-                                   : static_cast<const T*>(p.in[3]) + (t0 + t) * p.ld;
-            rr[i] = load8(src_row + static_cast<int64_t>(h) * kHead + row0 + c);
-        }
+    const int rt = pt / (ROWS / 8), rc = (pt % (ROWS / 8)) * 8;
+    if (rt < nt) {
+        const T* rows = REV ? static_cast<const T*>(p.dy) + (t0 + rt) * p.H * kHead
+                            : static_cast<const T*>(p.in[3]) + (t0 + rt) * p.ld;
+        raw.row = load8(rows + head + row0 + rc);
     }
+}
+// ... and, converted, from there into a stage.
+template <typename T, int ROWS, bool REV>
+__device__ __forceinline__ void stage_chunk(Stage<ROWS, REV>& st, const Raw<T, ROWS, REV>& raw, int nt, int pt) {
+    const int t = pt >> 3, c = (pt & 7) * 8;
+    const auto put = [](float* to, const float* f) {
+        reinterpret_cast<float4*>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    };
+    float f[8];
+    if (t < nt) {
 #pragma unroll
-    for (int v = 0; v < nvec(REV); ++v) {
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            const int piece = pt + i * NPW * 32, t = piece >> 3, c = (piece & 7) * 8;
-            if (t >= nt) continue;
-            float f[8];
-            cvt8<T>(raw[v][i], f);
+        for (int v = 0; v < nvec(REV); ++v) {
+            cvt8<T>(raw.vec[v], f);
             if (v == 0) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = decay_m1(f[j]);
             }
-            float4* dst = reinterpret_cast<float4*>(&st.vec[v][t][c]);
-            dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-            dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+            put(&st.vec[v][t][c], f);
         }
     }
-#pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-        const int piece = pt + i * NPW * 32, t = piece / (ROWS / 8), c = (piece % (ROWS / 8)) * 8;
-        if (t >= nt) continue;
-        float f[8];
-        cvt8<T>(rr[i], f);
-        float4* dst = reinterpret_cast<float4*>(&st.row[t][c]);
-        dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-        dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+    const int rt = pt / (ROWS / 8), rc = (pt % (ROWS / 8)) * 8;
+    if (rt < nt) {
+        cvt8<T>(raw.row, f);
+        put(&st.row[rt][rc], f);
     }
 }
 
@@ -124,16 +119,24 @@ __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_scan_kernel(const TmixA
     const auto tokens_in = [&](int c) { return min(CT, hi - lo - c * CT); };
 
     if (warp >= NCW) {                       // producers
+        // a chunk's loads are issued one chunk ahead of its conversion
         const int pt = threadIdx.x - NCW * 32;
-        if (nchunk > 0) fill<T, ROWS, REV>(p, sm.st[0], lo + static_cast<int64_t>(chunk_of(0)) * CT,
-                                           tokens_in(chunk_of(0)), h, row0, pt);
+        Raw<T, ROWS, REV> raw;
+        const auto load = [&](int c) {
+            if (c < nchunk)
+                load_chunk<T, ROWS, REV>(p, raw, lo + static_cast<int64_t>(chunk_of(c)) * CT, tokens_in(chunk_of(c)),
+                                         h, row0, pt);
+        };
+        const auto stage = [&](int c) {
+            if (c < nchunk) stage_chunk<T, ROWS, REV>(sm.st[c & 1], raw, tokens_in(chunk_of(c)), pt);
+        };
+        load(0);
+        stage(0);
+        load(1);
         __syncthreads();
         for (int c = 0; c < nchunk; ++c) {
-            if (c + 1 < nchunk) {
-                const int n = chunk_of(c + 1);
-                fill<T, ROWS, REV>(p, sm.st[(c + 1) & 1], lo + static_cast<int64_t>(n) * CT, tokens_in(n), h,
-                                   row0, pt);
-            }
+            stage(c + 1);
+            load(c + 2);
             if constexpr (!REV) {
                 if (c > 0) store_y<T, ROWS>(p, sm.y[(c - 1) & 1], lo + static_cast<int64_t>(c - 1) * CT, CT, h,
                                             row0, pt);
@@ -283,16 +286,19 @@ template <typename T, int RPL, int NCW, bool REV>
 cudaError_t launch_scan(const TmixArgs& a, cudaStream_t s) {
     constexpr int ROWS = NCW * 8 * RPL;
     constexpr size_t smem = sizeof(Smem<ROWS, REV>);
-    auto kern = tmix_scan_kernel<T, RPL, NCW, REV>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<tmix_scan_kernel<T, RPL, NCW, REV>>(smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.S * a.H * (kHead / ROWS), (NCW + NPW) * 32, smem, s>>>(a);
+    tmix_scan_kernel<T, RPL, NCW, REV><<<a.S * a.H * (kHead / ROWS), (NCW + NPW) * 32, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T, bool REV>
 cudaError_t scan_by_size(const TmixArgs& a, cudaStream_t s) {
-    return launch_scan<T, 2, 4, REV>(a, s);
+#ifndef VAR_RPL
+#define VAR_RPL 2
+#define VAR_NCW 4
+#endif
+    return launch_scan<T, VAR_RPL, VAR_NCW, REV>(a, s);
 }
 
 // ------------------------------------------------------------ single token --

@@ -13,6 +13,7 @@
 #include <cstdint>
 
 #include "rq_internal.h"
+#include "rq_once.h"
 
 namespace rq {
 
@@ -121,12 +122,26 @@ __device__ __forceinline__ T from_f32(float v) {
 }
 
 // ------------------------------------------------------------------- decay --
-__device__ __forceinline__ float decay_gate(float d) { return 1.f / (1.f + expf(-d)); }
-__device__ __forceinline__ float decay_log(float d) { return -kDecay * decay_gate(d); }
+// sigmoid(d), relative error about 2^-21.5 (the hardware's 2^x and 1/x are good
+// to 2^-22 and 2^-23): it scales log w, so the state's error stays below that.
+__device__ __forceinline__ float decay_gate(float d) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    return s;
+}
 // w - 1: the update w S = S + (w - 1) S then rounds S once, and a decay near 1
 // keeps its distance from 1 over thousands of steps (w itself, rounded to 24
 // bits, would be off by up to 2^-25 in every step, in the same direction).
-__device__ __forceinline__ float decay_m1(float d) { return expm1f(decay_log(d)); }
+// e^x - 1 by its series x (1 + x/2 (1 + x/3 (...))): -0.61 <= x <= 0, so ten
+// terms leave less than 0.61^10 / 11! < 2^-32 of it.
+__device__ __forceinline__ float decay_m1(float d) {
+    const float x = -kDecay * decay_gate(d);
+    float p = fmaf(x, 1.f / 10.f, 1.f);
+#pragma unroll
+    for (int n = 9; n >= 2; --n) p = fmaf(x * p, 1.f / n, 1.f);
+    return x * p;
+}
 
 // --------------------------------------------------------------- sequences --
 // Tokens [lo, hi) of sequence i; false (and a status) for offsets that are

@@ -379,12 +379,10 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
 
 template <typename T>
 cudaError_t launch(const TmixArgs& a, cudaStream_t s) {
-    auto kern = tmix_chunk_bwd_kernel<T>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+    const cudaError_t e = allow_smem<tmix_chunk_bwd_kernel<T>>(sizeof(Smem));
     if (e != cudaSuccess) return e;
     const int64_t places = a.T / C + a.S;
-    kern<<<static_cast<unsigned>(places * a.H), THREADS, sizeof(Smem), s>>>(a);
+    tmix_chunk_bwd_kernel<T><<<static_cast<unsigned>(places * a.H), THREADS, sizeof(Smem), s>>>(a);
     return cudaGetLastError();
 }
 

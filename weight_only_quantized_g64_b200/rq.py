@@ -81,9 +81,7 @@ def lib():
     L.rq_gemv_p8_g16.restype = i32
     L.rq_gemv_p4a_g32.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp]
     L.rq_gemv_p4a_g32.restype = i32
-    L.rq_lora_work_bytes.argtypes = [i64, i64, i64]
-    L.rq_lora_work_bytes.restype = ctypes.c_size_t
-    L.rq_lora_add.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, i64, i32, i32, vp, vp, vp]
+    L.rq_lora_add.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, i64, i32, i32, vp, vp]
     L.rq_lora_add.restype = i32
     f32 = ctypes.c_float
     L.rq_norm_residual.argtypes = [vp, i64, i64, i64, i32, i32, i64, vp, vp, f32, vp, i64, vp, i64, i32, vp, vp, i32,
@@ -338,16 +336,21 @@ def rkv_fused(x: torch.Tensor, wr, wk, wv, N: int, bits: int, ys=None, stream=No
 HEAD = 64
 
 
+_this_device = torch._C._cuda_getDevice
+_stream_of = torch._C._cuda_getCurrentRawStream      # of a device: the stream's handle alone
+_REAL = {torch.float32: OUT_F32, torch.float16: OUT_F16}
+
+
 def _placed(fn):
     """The call runs, and allocates, on its first tensor's device and on the
     given stream (default: that device's current one)."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         first = args[0] if args else next(iter(kw.values()), None)
-        if not isinstance(first, torch.Tensor) or not first.is_cuda or (
-                stream is None and first.device.index == torch.cuda.current_device()):
+        at = first.get_device() if isinstance(first, torch.Tensor) else -1
+        if at < 0 or (stream is None and at == _this_device()):
             return fn(*args, **kw)
-        with torch.cuda.device(first.device), torch.cuda.stream(stream):
+        with torch.cuda.device(at), torch.cuda.stream(stream):
             return fn(*args, **kw)
     return call
 
@@ -357,21 +360,18 @@ def _need(ok: bool, what: str, status: int = ERR_SHAPE):
         raise RQError(status, what)
 
 
-def _tensor(call: str, name: str, t, dtype, shape, like=None):
-    """t is a contiguous tensor of this type and shape (and on like's device)."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _tensor(call: str, name: str, t, dtype, shape, at: int):
+    """t is a contiguous tensor of this type and shape on device number `at` (-1: the host)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise RQError(ERR_SHAPE, f"{call}: {name} must be a contiguous {dtype} {tuple(shape)}, "
                                  f"not {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
-    if like is not None and t.device != like.device:
-        raise RQError(ERR_SHAPE, f"{call}: {name} is on {t.device}, not on {like.device}")
+    if t.get_device() != at:
+        raise RQError(ERR_SHAPE, f"{call}: {name} is on {t.device}, not with the first tensor")
 
 
-def _on_gpu(call: str, t):
-    if not t.is_cuda:
-        raise RQError(ERR_SHAPE, f"{call}: the tensors must be on a CUDA device, not on {t.device}")
-
-
-_REAL = {torch.float32: OUT_F32, torch.float16: OUT_F16}
+def _on_gpu(call: str, at: int):
+    if at < 0:
+        raise RQError(ERR_SHAPE, f"{call}: the tensors must be on a CUDA device, not on the host")
 
 
 @_placed
@@ -380,25 +380,33 @@ def lora_add(x, A, B, ids, y, out=None, ranks=None, scale=None, epilogue: int = 
     [M, K], A fp16 [L, R, K], B fp16 [L, N, R], ids int32 [M] (negative: none),
     ranks int32 [L], scale fp32 [L].  out may be y."""
     c = "rq_lora_add"
-    _need(x.dim() == 2 and A.dim() == 3 and B.dim() == 3, f"{c}: x [M, K], A [L, R, K] and B [L, N, R] are needed")
+    if x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise RQError(ERR_SHAPE, f"{c}: x [M, K], A [L, R, K] and B [L, N, R] are needed")
     (M, K), (L, R), N = x.shape, A.shape[:2], B.shape[1]
-    _need(y.dtype in _REAL, f"{c}: y must be float32 or float16, not {y.dtype}", ERR_RANGE)
-    _tensor(c, "x", x, torch.float16, (M, K))
-    _tensor(c, "A", A, torch.float16, (L, R, K), x)
-    _tensor(c, "B", B, torch.float16, (L, N, R), x)
-    _tensor(c, "ids", ids, torch.int32, (M,), x)
-    _tensor(c, "y", y, y.dtype, (M, N), x)
-    for name, t, dtype, shape in (("out", out, y.dtype, (M, N)), ("ranks", ranks, torch.int32, (L,)),
-                                  ("scale", scale, torch.float32, (L,)), ("dev_status", dev_status, torch.int32, (1,))):
-        if t is not None:
-            _tensor(c, name, t, dtype, shape, x)
-    _on_gpu(c, x)
+    at, dtype = x.get_device(), y.dtype
+    if dtype not in _REAL:
+        raise RQError(ERR_RANGE, f"{c}: y must be float32 or float16, not {dtype}")
+    _tensor(c, "x", x, torch.float16, (M, K), at)
+    _tensor(c, "A", A, torch.float16, (L, R, K), at)
+    _tensor(c, "B", B, torch.float16, (L, N, R), at)
+    _tensor(c, "ids", ids, torch.int32, (M,), at)
+    _tensor(c, "y", y, dtype, (M, N), at)
+    if ranks is not None:
+        _tensor(c, "ranks", ranks, torch.int32, (L,), at)
+    if scale is not None:
+        _tensor(c, "scale", scale, torch.float32, (L,), at)
+    if dev_status is not None:
+        _tensor(c, "dev_status", dev_status, torch.int32, (1,), at)
+    if out is not None:
+        _tensor(c, "out", out, dtype, (M, N), at)
+    if at < 0:
+        _on_gpu(c, at)
     if out is None:
         out = torch.empty_like(y)
-    n = 0 if M <= MAX_DECODE_M else int(lib().rq_lora_work_bytes(M, K, R))
-    work = torch.empty(n // 4, dtype=torch.float32, device=x.device) if n else None
-    _check(lib().rq_lora_add(_p(x), M, K, _p(A), _p(B), L, R, _p(ids), _p(ranks), _p(scale), _p(y), _p(out), N,
-                             _REAL[y.dtype], epilogue, _p(work), _p(dev_status), _stream()), c)
+    st = lib().rq_lora_add(x.data_ptr(), M, K, A.data_ptr(), B.data_ptr(), L, R, ids.data_ptr(), _p(ranks), _p(scale),
+                           y.data_ptr(), out.data_ptr(), N, _REAL[dtype], epilogue, _p(dev_status), _stream_of(at))
+    if st != OK:
+        raise RQError(st, c)
     return out
 
 
@@ -415,69 +423,83 @@ def norm_residual(y, post: str = "none", post_group: int = 0, post_weight=None, 
     (rows may be columns of a wider matrix), h [M, D]; weights, biases and alpha
     fp32 [D].  Returns (h', x); h' is None without h and h_out.  h_out may be h."""
     c = "rq_norm_residual"
-    _need(y.dim() == 2, f"{c}: y must be [M, D], not {tuple(y.shape)}")
-    _need(y.dtype in _REAL, f"{c}: y must be float32 or float16, not {y.dtype}", ERR_RANGE)
-    _need(post in NORMS and pre in NORMS and gate_act in GATES, f"{c}: {post}, {pre} or {gate_act} is not known",
-          ERR_RANGE)
-    M, D = y.shape
-    ld = [D, D, D]
-    for i, (name, t) in enumerate((("y", y), ("add", add), ("gate", gate))):
+    at, dtype, shape = y.get_device(), y.dtype, y.shape
+    if len(shape) != 2:
+        raise RQError(ERR_SHAPE, f"{c}: y must be [M, D], not {tuple(shape)}")
+    if dtype not in _REAL:
+        raise RQError(ERR_RANGE, f"{c}: y must be float32 or float16, not {dtype}")
+    if post not in NORMS or pre not in NORMS or gate_act not in GATES:
+        raise RQError(ERR_RANGE, f"{c}: {post}, {pre} or {gate_act} is not known")
+    M, D = shape
+
+    def rows(name, t):
+        st = t.stride()
+        if t.dtype is not dtype or t.shape != shape or st[1] != 1 or t.get_device() != at:
+            raise RQError(ERR_SHAPE, f"{c}: {name} must be {dtype} {(M, D)} on {y.device} with rows of stride 1, "
+                                     f"not {t.dtype} {tuple(t.shape)} {st} on {t.device}")
+        return st[0] if M > 1 else D
+
+    ld_y = rows("y", y)
+    ld_add = rows("add", add) if add is not None else D
+    ld_gate = rows("gate", gate) if gate is not None else D
+    if h is not None:
+        _tensor(c, "h", h, dtype, shape, at)
+    if h_out is not None:
+        _tensor(c, "h_out", h_out, dtype, shape, at)
+    if x is not None:
+        _tensor(c, "x", x, torch.float16, shape, at)
+    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("alpha", alpha),
+                    ("pre_weight", pre_weight), ("pre_bias", pre_bias)):
         if t is not None:
-            if t.dtype != y.dtype or t.shape != y.shape or t.stride(1) != 1 or t.device != y.device:
-                raise RQError(ERR_SHAPE, f"{c}: {name} must be {y.dtype} {(M, D)} on {y.device} with rows of stride 1, "
-                                         f"not {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
-            if M > 1:
-                ld[i] = t.stride(0)
-    for name, t, dtype, shape in (("h", h, y.dtype, (M, D)), ("h_out", h_out, y.dtype, (M, D)),
-                                  ("x", x, torch.float16, (M, D)), ("post_weight", post_weight, torch.float32, (D,)),
-                                  ("post_bias", post_bias, torch.float32, (D,)), ("alpha", alpha, torch.float32, (D,)),
-                                  ("pre_weight", pre_weight, torch.float32, (D,)),
-                                  ("pre_bias", pre_bias, torch.float32, (D,))):
-        if t is not None:
-            _tensor(c, name, t, dtype, shape, y)
-    _on_gpu(c, y)
+            _tensor(c, name, t, torch.float32, (D,), at)
+    if at < 0:
+        _on_gpu(c, at)
     if h_out is None and h is not None:
         h_out = torch.empty_like(h)
     if x is None:
-        x = torch.empty((M, D), dtype=torch.float16, device=y.device)
-    _check(lib().rq_norm_residual(_p(y), ld[0], M, D, _REAL[y.dtype], NORMS[post], post_group, _p(post_weight),
-                                  _p(post_bias), eps_post, _p(add), ld[1], _p(gate), ld[2], GATES[gate_act], _p(h),
-                                  _p(alpha), NORMS[pre], _p(pre_weight), _p(pre_bias), eps_pre, _p(h_out), _p(x),
-                                  _stream()), c)
+        x = torch.empty(shape, dtype=torch.float16, device=y.device)
+    st = lib().rq_norm_residual(y.data_ptr(), ld_y, M, D, _REAL[dtype], NORMS[post], post_group, _p(post_weight),
+                                _p(post_bias), eps_post, _p(add), ld_add, _p(gate), ld_gate, GATES[gate_act], _p(h),
+                                _p(alpha), NORMS[pre], _p(pre_weight), _p(pre_bias), eps_pre, _p(h_out), x.data_ptr(),
+                                _stream_of(at))
+    if st != OK:
+        raise RQError(st, c)
     return h_out, x
 
 
 def _heads(call: str, names: str, tensors):
-    """Checks the [T, H, 64] inputs of one call -> (T, H, row stride)."""
+    """Checks the [T, H, 64] inputs of one call -> (T, H, row stride, device number)."""
     x = tensors[0]
-    _need(x.dim() == 3 and x.shape[2] == HEAD, f"{call}: {names[0]} must be [T, H, {HEAD}], not {tuple(x.shape)}")
-    _need(x.dtype in _REAL, f"{call}: {names[0]} must be float32 or float16, not {x.dtype}", ERR_RANGE)
-    T, H = x.shape[0], x.shape[1]
-    ld = x.stride(0) if T > 1 else H * HEAD
+    shape, stride, at, dtype = x.shape, x.stride(), x.get_device(), x.dtype
+    if len(shape) != 3 or shape[2] != HEAD:
+        raise RQError(ERR_SHAPE, f"{call}: {names[0]} must be [T, H, {HEAD}], not {tuple(shape)}")
+    if dtype not in _REAL:
+        raise RQError(ERR_RANGE, f"{call}: {names[0]} must be float32 or float16, not {dtype}")
+    T, H = shape[0], shape[1]
+    ld = stride[0] if T > 1 else H * HEAD
     for n, t in zip(names, tensors):
-        if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
-            raise RQError(ERR_SHAPE, f"{call}: {n} must be {x.dtype} {tuple(x.shape)} on {x.device} like {names[0]}, "
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != at:
+            raise RQError(ERR_SHAPE, f"{call}: {n} must be {dtype} {tuple(shape)} on {x.device} like {names[0]}, "
                                      f"not {t.dtype} {tuple(t.shape)} on {t.device}")
-        if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != HEAD) or (T > 1 and t.stride(0) != ld)):
-            raise RQError(ERR_SHAPE, f"{call}: {n} must have strides ({ld}, {HEAD}, 1), not {t.stride()}")
-    return T, H, ld
+        st = t.stride()
+        if st != (ld, HEAD, 1) and t.numel() and (
+                st[2] != 1 or (H > 1 and st[1] != HEAD) or (T > 1 and st[0] != ld)):
+            raise RQError(ERR_SHAPE, f"{call}: {n} must have strides ({ld}, {HEAD}, 1), not {st}")
+    return T, H, ld, at
 
 
-def _states(call: str, x, S: int, H: int, state, state_out, slots, dev_status):
+def _states(call: str, at: int, S: int, H: int, state, state_out, slots, dev_status):
     """Checks states and slots -> the number of states."""
     n = S
+    if slots is not None:
+        _tensor(call, "slots", slots, torch.int32, (S,), at)
+        _need(state is not None or state_out is not None, f"{call}: slots without a state")
+        n = (state if state is not None else state_out).shape[0]
     for name, t in (("state", state), ("state_out", state_out)):
         if t is not None:
-            if slots is not None and t.dim() == 4:
-                n = t.shape[0]
-            _tensor(call, name, t, torch.float32, (n, H, HEAD, HEAD), x)
-    if slots is not None:
-        _tensor(call, "slots", slots, torch.int32, (S,), x)
-        _need(state is not None or state_out is not None, f"{call}: slots without a state")
-        _need(state is None or state_out is None or state.shape == state_out.shape,
-              f"{call}: state and state_out must have the same shape")
+            _tensor(call, name, t, torch.float32, (n, H, HEAD, HEAD), at)
     if dev_status is not None:
-        _tensor(call, "dev_status", dev_status, torch.int32, dev_status.shape, x)
+        _tensor(call, "dev_status", dev_status, torch.int32, (1,), at)
     return n
 
 
@@ -498,22 +520,22 @@ def tmix_scan(r, d, k, v, a, b, seq_start, state=None, state_out=None, slots=Non
     slots int32 [S].  Returns (y, state_out); state_out may be state itself, is
     allocated when not given, and for a pool must be given."""
     c = "rq_tmix_scan"
-    T, H, ld = _heads(c, "rdkvab", (r, d, k, v, a, b))
+    T, H, ld, at = _heads(c, "rdkvab", (r, d, k, v, a, b))
     S = seq_start.numel() - 1
-    _tensor(c, "seq_start", seq_start, torch.int32, (max(S, 1) + 1,), r)
-    n = _states(c, r, S, H, state, state_out, slots, dev_status)
+    _tensor(c, "seq_start", seq_start, torch.int32, (max(S, 1) + 1,), at)
+    n = _states(c, at, S, H, state, state_out, slots, dev_status)
     if ckpt is not None:
-        _tensor(c, "ckpt", ckpt, torch.float32, (lib().rq_tmix_ckpt_bytes(T, S, H) // 4,), r)
+        _tensor(c, "ckpt", ckpt, torch.float32, (lib().rq_tmix_ckpt_bytes(T, S, H) // 4,), at)
     if y is not None:
-        _tensor(c, "y", y, r.dtype, (T, H, HEAD), r)
-    _on_gpu(c, r)
+        _tensor(c, "y", y, r.dtype, (T, H, HEAD), at)
+    _on_gpu(c, at)
     if y is None:
         y = torch.empty((T, H, HEAD), dtype=r.dtype, device=r.device)
     if state_out is None and slots is None:
         state_out = torch.empty((S, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
     _check(lib().rq_tmix_scan(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), T, H, ld, _REAL[r.dtype], _p(seq_start), S,
                               _p(state), _p(state_out), _p(slots), n, _p(y), _p(ckpt), _p(dev_status),
-                              _stream()), c)
+                              _stream_of(at)), c)
     return y, state_out
 
 
@@ -524,15 +546,15 @@ def tmix_scan_bwd(r, d, k, v, a, b, seq_start, ckpt, dy, dstate_out=None, grads=
     [T, H, 64] and dstate_out [S, H, 64, 64] (None: zeros).  Returns ((dr, dd,
     dk, dv, da, db), dstate)."""
     c = "rq_tmix_scan_bwd"
-    T, H, ld = _heads(c, "rdkvab", (r, d, k, v, a, b))
+    T, H, ld, at = _heads(c, "rdkvab", (r, d, k, v, a, b))
     S = seq_start.numel() - 1
-    _tensor(c, "seq_start", seq_start, torch.int32, (max(S, 1) + 1,), r)
-    _tensor(c, "ckpt", ckpt, torch.float32, (lib().rq_tmix_ckpt_bytes(T, S, H) // 4,), r)
-    _tensor(c, "dy", dy, r.dtype, (T, H, HEAD), r)
-    _states(c, r, S, H, dstate_out, dstate, None, dev_status)
+    _tensor(c, "seq_start", seq_start, torch.int32, (max(S, 1) + 1,), at)
+    _tensor(c, "ckpt", ckpt, torch.float32, (lib().rq_tmix_ckpt_bytes(T, S, H) // 4,), at)
+    _tensor(c, "dy", dy, r.dtype, (T, H, HEAD), at)
+    _states(c, at, S, H, dstate_out, dstate, None, dev_status)
     for i, g in enumerate(grads or ()):
-        _tensor(c, f"grads[{i}]", g, r.dtype, (T, H, HEAD), r)
-    _on_gpu(c, r)
+        _tensor(c, f"grads[{i}]", g, r.dtype, (T, H, HEAD), at)
+    _on_gpu(c, at)
     if grads is None:
         grads = tuple(torch.empty((T, H, HEAD), dtype=r.dtype, device=r.device) for _ in range(6))
     if dstate is None:
@@ -540,7 +562,7 @@ def tmix_scan_bwd(r, d, k, v, a, b, seq_start, ckpt, dy, dstate_out=None, grads=
     work = torch.empty_like(ckpt)
     _check(lib().rq_tmix_scan_bwd(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), T, H, ld, _REAL[r.dtype],
                                   _p(seq_start), S, _p(ckpt), _p(dy), _p(dstate_out), _p(dstate),
-                                  *(_p(g) for g in grads), _p(work), _p(dev_status), _stream()), c)
+                                  *(_p(g) for g in grads), _p(work), _p(dev_status), _stream_of(at)), c)
     return tuple(grads), dstate
 
 
@@ -549,17 +571,17 @@ def tmix_step(r, d, k, v, a, b, state=None, state_out=None, slots=None, y=None, 
     """One token of the time-mix recurrence for each of B sequences: r .. b fp32
     or fp16 [B, H, 64]; state as in tmix_scan.  Returns (y, state_out)."""
     c = "rq_tmix_step"
-    B, H, ld = _heads(c, "rdkvab", (r, d, k, v, a, b))
-    n = _states(c, r, B, H, state, state_out, slots, dev_status)
+    B, H, ld, at = _heads(c, "rdkvab", (r, d, k, v, a, b))
+    n = _states(c, at, B, H, state, state_out, slots, dev_status)
     if y is not None:
-        _tensor(c, "y", y, r.dtype, (B, H, HEAD), r)
-    _on_gpu(c, r)
+        _tensor(c, "y", y, r.dtype, (B, H, HEAD), at)
+    _on_gpu(c, at)
     if y is None:
         y = torch.empty((B, H, HEAD), dtype=r.dtype, device=r.device)
     if state_out is None and slots is None:
         state_out = torch.empty((B, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
     _check(lib().rq_tmix_step(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), B, H, ld, _REAL[r.dtype], _p(state),
-                              _p(state_out), _p(slots), n, _p(y), _p(dev_status), _stream()), c)
+                              _p(state_out), _p(slots), n, _p(y), _p(dev_status), _stream_of(at)), c)
     return y, state_out
 
 
