@@ -346,16 +346,18 @@ rq_status rq_gemm_wq(const uint16_t *x, int64_t M, int64_t K, const void *codes,
  * RQ_OUT_F16); out may be y itself, else they must not overlap.  epilogue:
  * RQ_EPI_NONE or RQ_EPI_RELU_SQ (the squared ReLU then comes here, not in the
  * product before).  Bad dtype or epilogue: RQ_ERR_RANGE.  K % 8 == 0, R % 8 ==
- * 0, 8 <= R <= RQ_MAX_LORA_RANK, 1 <= M < 2^24, any N >= 1, else
- * RQ_ERR_SHAPE.  Tokens of one request need not be neighbours, but tiles of
- * neighbours are faster.  Needs no workspace; deterministic; asynchronous on
- * `stream`.
+ * 0, 8 <= R <= RQ_MAX_LORA_RANK, 1 <= M <= 4194240, any N >= 1, else
+ * RQ_ERR_SHAPE.  work: rq_lora_work_bytes(M, R) bytes, 16-byte aligned (0 bytes,
+ * NULL allowed, for M <= RQ_MAX_DECODE_M); two calls that may overlap need two.
+ * Tokens of one request need not be neighbours, but neighbours are faster.
+ * Deterministic; asynchronous on `stream`; allocates nothing.
  */
 #define RQ_MAX_LORA_RANK 128
+size_t rq_lora_work_bytes(int64_t M, int64_t R);
 rq_status rq_lora_add(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A, const uint16_t *B,
                       int64_t L, int64_t R, const int32_t *ids, const int32_t *ranks,
                       const float *scale, const void *y, void *out, int64_t N, int dtype, int epilogue,
-                      int *dev_status, rq_stream_t stream);
+                      void *work, int *dev_status, rq_stream_t stream);
 
 /*
  * rq_norm_residual -- the step between two projections, in one pass:

@@ -111,7 +111,7 @@ def test_tmix_binding_refuses(L):
 
 def lora_args(**kw):
     a = dict(x=FAKE, M=40, K=64, A=FAKE, B=FAKE, L=2, R=16, ids=FAKE, ranks=None, scale=None, y=FAKE, out=FAKE, N=33,
-             dtype=0, epi=0, status=None, stream=None)
+             dtype=0, epi=0, work=FAKE, status=None, stream=None)
     a.update(kw)
     return list(a.values())
 
@@ -120,15 +120,18 @@ def test_lora_argument_errors(L):
     f = L.rq_lora_add
     for bad in (dict(dtype=2), dict(dtype=-1), dict(epi=2), dict(epi=-1)):
         assert f(*lora_args(**bad)) == rq.ERR_RANGE, bad
-    for bad in (dict(M=0), dict(M=1 << 24), dict(K=0), dict(K=12), dict(N=0), dict(N=1 << 31), dict(L=0), dict(R=0),
+    for bad in (dict(M=0), dict(M=4194241), dict(K=0), dict(K=12), dict(N=0), dict(N=1 << 31), dict(L=0), dict(R=0),
                 dict(R=12), dict(R=136)):
         assert f(*lora_args(**bad)) == rq.ERR_SHAPE, bad
-    for n in ("x", "A", "B", "ids", "y", "out"):
+    for n in ("x", "A", "B", "ids", "y", "out", "work"):
         assert f(*lora_args(**{n: None})) == rq.ERR_NULL, n
-    for n in ("x", "A", "B", "y", "out"):
+    for n in ("x", "A", "B", "y", "out", "work"):
         assert f(*lora_args(**{n: FAKE + 8})) == rq.ERR_ALIGN, n
     for n in ("ids", "ranks", "scale", "status"):
         assert f(*lora_args(**{n: FAKE + 2})) == rq.ERR_ALIGN, n
+    assert L.rq_lora_work_bytes(32, 64) == 0
+    assert L.rq_lora_work_bytes(33, 64) == 3 * (4 * 1024 + 64)
+    assert L.rq_lora_work_bytes(33, 12) == 0
 
 
 def test_lora_binding_refuses(L):

@@ -1,20 +1,26 @@
 // rq_lora.cu -- low-rank adapters of many requests beside one product:
 //   out[m] = epi(y[m] + s_a B_a (A_a x[m])),   a = ids[m].
 //
-// One launch either way: a cluster of CTAs splits K for A x, exchanges the R
-// sums of each token through distributed shared memory, and splits N for B.
-//
-// Few tokens (decode): a cluster of 8 per token, plain fp32 sums.  Its part of
-// B (one contiguous piece) is sent for into L2 at the start, and its first rows
-// into registers before the cluster meets.  Bound by latency: two dependent
-// reads of memory and a barrier.
-//
-// Many tokens (prefill): a cluster per 64 tokens on the warp-level tensor
-// cores.  The products of A x are exact in fp32; for B each fp32 sum t is split
+// Products with B run on the warp-level tensor cores with each fp32 sum t split
 // into two fp16 parts, t = 2^-e (hi + lo), scaled per token so that the largest
-// lies near 2^14, so 22 bits of it enter the product.  Bound by the bytes of x,
-// y and out.  A tile whose tokens use several adapters takes them in turn and
-// keeps each token's own.
+// lies near 2^14: 22 bits of it enter the product, whose terms are exact.  All
+// operands go into the MMAs as they come from memory, 16 bytes of a row per
+// lane: the order of the summed index does not matter as long as both operands
+// follow it.
+//
+// Few tokens (decode): one launch, a cluster of 8 CTAs per token.  Each takes an
+// eighth of K for A x (plain fp32 sums), sends its R sums to all eight, and
+// after one cluster barrier takes an eighth of the outputs; hi and lo are two of
+// the eight columns of an MMA over 16 rows of B, the first of which are on their
+// way before the cluster meets.  Bound by latency: two dependent reads of memory
+// and a barrier.
+//
+// Many tokens (prefill): two launches.  A CTA per 16 tokens splits K over its
+// warps for A x and leaves hi and lo of t in the order of the MMA's registers;
+// then every warp of a second launch takes 16 tokens x 64 outputs without shared
+// memory or barriers, its y and B on their way before the first launch has
+// ended.  Bound by the bytes of x, y and out.  Tokens of several adapters in a
+// warp's 16 are taken in turn, and each keeps its own sum.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -66,6 +72,56 @@ __device__ __forceinline__ float dot8(const uint4& a, const float* b, float c) {
     return c;
 }
 
+// The power of two 2^e that brings a largest magnitude into [2^14, 2^15).
+__device__ __forceinline__ int scale_of(float top) {
+    const int ex = static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127;
+    return top > 0.f ? min(14 - ex, 100) : 0;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+// The first or the second fp16 part of f; an infinite one has no rest.
+__device__ __forceinline__ __half split(float f, int part) {
+    const __half h = __float2half_rn(f);
+    if (part == 0) return h;
+    return __float2half_rn(fabsf(f) <= 65504.f ? f - __half2float(h) : 0.f);
+}
+__device__ __forceinline__ void mma(float c[4], const uint32_t a[4], const uint32_t b[2]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// The order of the ranks in the MMAs with B, R <= 8 PR: register j of a row holds, in lane (g, q), this rank and the
+// next: 2 ranks of 8, 4 of 16 in a lane, or 8 (16 bytes) of every 32.
+template <int PR>
+__device__ __forceinline__ int rank_at(int q, int j) {
+    return PR == 1 ? 2 * q + 8 * j : PR == 2 ? 4 * q + 2 * j : 8 * q + 8 * (j & ~3) + 2 * (j & 3);
+}
+// Those registers of one row of B (from: the row at rank_at(q, 0)), zeros where it is not live or behind the rank.
+template <int PR>
+__device__ __forceinline__ void row_of_b(const uint16_t* from, bool live, int rank0, int rank, uint32_t* r) {
+    if constexpr (PR == 1) r[0] = live && rank0 < rank ? __ldg(reinterpret_cast<const uint32_t*>(from)) : 0u;
+    if constexpr (PR == 2) {
+        const uint2 v = live && rank0 < rank ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0u, 0u);
+        r[0] = v.x;
+        r[1] = v.y;
+    }
+    if constexpr (PR >= 4) {
+#pragma unroll
+        for (int j = 0; j < PR; j += 4) {    // 32 ranks further every 4 registers
+            const uint4 v = live && rank0 + 8 * j < rank ? __ldg(reinterpret_cast<const uint4*>(from + 8 * j))
+                                                         : make_uint4(0u, 0u, 0u, 0u);
+            r[j] = v.x;
+            r[j + 1] = v.y;
+            r[j + 2] = v.z;
+            r[j + 3] = v.w;
+        }
+    }
+}
+// Ranks behind the adapter's own are not its: what B holds there does not count.
+__device__ __forceinline__ uint32_t keep_of(int r, int rank) {
+    return r + 1 < rank ? 0xffffffffu : r < rank ? 0xffffu : 0u;
+}
+
 // ------------------------------------------------------------- few tokens --
 constexpr int CS = 8;                        // CTAs of a token
 constexpr int TT = 256;                      // threads
@@ -87,11 +143,6 @@ __global__ void __launch_bounds__(TT) lora_token_kernel(const LoraArgs p) {
         return;
     }
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-    if (threadIdx.x == 0 && n1 > n0) {
-        const char* from = reinterpret_cast<const char*>(p.B + (static_cast<int64_t>(a) * p.N + n0) * p.R);
-        const uint32_t size = static_cast<uint32_t>(min((n1 - n0) * p.R * 2, int64_t{1} << 20));
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(size) : "memory");
-    }
 
     // A x over this CTA's part of K; warp w takes ranks w, w + 8, ...
     const int rank = rank_of(p, a);
@@ -122,21 +173,31 @@ __global__ void __launch_bounds__(TT) lora_token_kernel(const LoraArgs p) {
         for (int r = 0; r < PR; ++r) acc[r] = dot8(w[r], xf, acc[r]);
     }
 
-    // the first rows of B and y, while the sums are joined
-    constexpr int ROWS = TT / PR, AHEAD = 4;
-    const int piece = threadIdx.x % PR;
-    const uint4* bp = reinterpret_cast<const uint4*>(p.B) + static_cast<int64_t>(a) * p.N * (p.R / 8) + piece;
-    const int64_t first = n0 + threadIdx.x / PR;
-    const auto row_of_b = [&](int64_t n) {
-        return n < n1 && piece * 8 < rank ? __ldg(bp + n * (p.R / 8)) : make_uint4(0u, 0u, 0u, 0u);
+    // the first rows of B and y, while the sums are joined.  A warp takes 32 outputs at a time: two MMAs of 16 rows;
+    // lane (g, q) supplies rows g and g + 8 of each, and for the ranks that its registers hold the same of t
+    constexpr int NR = PR;
+    constexpr int AHEAD = PR <= 4 ? 2 : 1;
+    const int g = lane >> 2, q = lane & 3;
+    const int rank0 = rank_at<PR>(q, 0);
+    const uint16_t* bp = p.B + static_cast<int64_t>(a) * p.N * p.R + rank0;
+    const bool ragged = rank < 8 * PR;
+    struct Rows {
+        uint32_t r[4][NR];                   // rows g, g + 8, g + 16, g + 24
+        float y;                             // of output `lane`
     };
-    uint4 bv[AHEAD];
-    float yv[AHEAD];
+    const auto rows_at = [&](int64_t n, Rows& w) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-        bv[i] = row_of_b(first + i * ROWS);
-        yv[i] = piece == 0 && first + i * ROWS < n1 ? get<T>(p.y, yrow + first + i * ROWS) : 0.f;
-    }
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = n + 8 * i + g;
+            row_of_b<PR>(bp + row * p.R, row < n1, rank0, rank, w.r[i]);
+        }
+        w.y = n + lane < n1 ? get<T>(p.y, yrow + n + lane) : 0.f;
+    };
+    constexpr int STEP = TT;                 // outputs that the CTA takes at a time
+    const int64_t first = n0 + 32 * warp;
+    Rows w[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) rows_at(first + i * STEP, w[i]);
 #pragma unroll
     for (int r = 0; r < PR; ++r)
 #pragma unroll
@@ -156,41 +217,59 @@ __global__ void __launch_bounds__(TT) lora_token_kernel(const LoraArgs p) {
         ts[threadIdx.x] = p.scale == nullptr ? t : t * p.scale[a];
     }
     __syncthreads();
-    float t[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = ts[piece * 8 + j];
-    // ranks behind the adapter's own are not its: neither their sums nor their columns of B count
-    const int tail = rank - piece * 8;
-    const auto row_sum = [&](uint4 b) {
-        if (tail > 0 && tail < 8) {
-            __half* h = reinterpret_cast<__half*>(&b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j >= tail) h[j] = __float2half_rn(0.f);
-        }
-        float s = tail > 0 ? dot8(b, t, 0.f) : 0.f;
-#pragma unroll
-        for (int o = 1; o < PR; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        return s;
-    };
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-        const float s = row_sum(bv[i]);
-        const int64_t n = first + i * ROWS;
-        if (piece == 0 && n < n1) put<T>(p.out, yrow + n, finish(yv[i] + s, p.relu_sq));
+    float top = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < PR * 8; ++r) {
+        const float mag = fabsf(ts[r]);
+        top = mag <= FLT_MAX ? fmaxf(top, mag) : top;            // infinities and NaN pass as they are
     }
-    for (int64_t base = n0 + AHEAD * ROWS; base < n1; base += AHEAD * ROWS) {
-        const int64_t at = base + threadIdx.x / PR;
+    const int e = scale_of(top);
+    const float up = pow2(e), back = pow2(-e);
+    uint32_t tf[NR], keep[NR];               // column 0 of the product: hi, column 1: lo
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            bv[i] = row_of_b(at + i * ROWS);
-            yv[i] = piece == 0 && at + i * ROWS < n1 ? get<T>(p.y, yrow + at + i * ROWS) : 0.f;
+    for (int j = 0; j < NR; ++j) {
+        const int r = rank_at<PR>(q, j);
+        __half2 v = __floats2half2_rn(0.f, 0.f);
+        if (g < 2) v = __halves2half2(split(ts[r] * up, g), split(ts[r + 1] * up, g));
+        tf[j] = *reinterpret_cast<const uint32_t*>(&v);
+        keep[j] = keep_of(r, rank);
+    }
+    const auto finish_rows = [&](int64_t n, Rows& w) {
+        float v[4];
+#pragma unroll
+        for (int pair = 0; pair < 2; ++pair) {
+            uint32_t(&lo)[NR] = w.r[2 * pair];
+            uint32_t(&hi)[NR] = w.r[2 * pair + 1];
+            if (ragged) {
+#pragma unroll
+                for (int j = 0; j < NR; ++j) {
+                    lo[j] &= keep[j];
+                    hi[j] &= keep[j];
+                }
+            }
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NR; j += 2) {
+                const uint32_t fa[4] = {lo[j], hi[j], NR > 1 ? lo[NR > 1 ? j + 1 : j] : 0u,
+                                        NR > 1 ? hi[NR > 1 ? j + 1 : j] : 0u};
+                const uint32_t fb[2] = {tf[j], NR > 1 ? tf[NR > 1 ? j + 1 : j] : 0u};
+                mma(c, fa, fb);
+            }
+            v[2 * pair] = c[0] + c[1];       // right in the lanes with q = 0
+            v[2 * pair + 1] = c[2] + c[3];
         }
 #pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], (lane & 7) * 4);
+        const float s = lane < 8 ? v[0] : lane < 16 ? v[1] : lane < 24 ? v[2] : v[3];
+        if (n + lane < n1) put<T>(p.out, yrow + n + lane, finish(fmaf(s, back, w.y), p.relu_sq));
+    };
+    for (int64_t n = first; n < n1; n += AHEAD * STEP) {
+#pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const float s = row_sum(bv[i]);
-            const int64_t n = at + i * ROWS;
-            if (piece == 0 && n < n1) put<T>(p.out, yrow + n, finish(yv[i] + s, p.relu_sq));
+            if (n + i * STEP < n1) {
+                finish_rows(n + i * STEP, w[i]);
+                rows_at(n + (AHEAD + i) * STEP, w[i]);
+            }
         }
     }
 }
@@ -212,48 +291,15 @@ cudaError_t launch_tokens(const LoraArgs& a, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------ many tokens --
-constexpr int TM = 64;                       // tokens of a tile
-constexpr int KT = 64;                       // k of a stage
-constexpr int NT = 128;                      // outputs of a tile
-constexpr int LDK = KT + 8;                  // halves; 16-byte pieces of 8 rows meet no bank twice
-constexpr int STAGES = 3;
+constexpr int TM = 16;                       // tokens of a tile
+constexpr int SW = 16;                       // warps that split K
 
-__device__ __forceinline__ void cp16(void* dst, const void* src, bool live) {
-    const int n = live ? 16 : 0;             // 0: the destination is filled with zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t r[4], const void* p) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(smem_u32(p)));
-}
-__device__ __forceinline__ void ldsm2(uint32_t r[2], const void* p) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
-                 : "=r"(r[0]), "=r"(r[1])
-                 : "r"(smem_u32(p)));
-}
-__device__ __forceinline__ void mma(float c[4], const uint32_t a[4], const uint32_t b[2]) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+// The smallest adapter of 16 tokens above `after` (INT_MAX: none); id: of token lane % 16.
+__device__ __forceinline__ int next_adapter(int id, int after) {
+    return __reduce_min_sync(0xffffffffu, id > after ? id : INT_MAX);
 }
 
-// The smallest adapter of the tile above `after` (INT_MAX: none); all threads.
-__device__ __forceinline__ int next_adapter(const int* ids, int after) {
-    const int lane = threadIdx.x & 31;
-    int best = INT_MAX;
-#pragma unroll
-    for (int i = lane; i < TM; i += 32) best = ids[i] > after ? min(best, ids[i]) : best;
-    return __reduce_min_sync(0xffffffffu, best);
-}
-
-// Four consecutive outputs of row m from column n on; `wide`: 4 | N.
+// Four consecutive outputs, `left` of them inside the row; `wide`: 4 | N.
 template <typename T>
 __device__ __forceinline__ void get4(const void* p, int64_t at, int64_t left, bool wide, float f[4]) {
     if (wide && left >= 4) {
@@ -288,274 +334,235 @@ __device__ __forceinline__ void put4(void* p, int64_t at, int64_t left, bool wid
         if (j < left) put<T>(p, at + j, f[j]);
 }
 
-// RT: tiles of 8 ranks (R <= 8 RT)
-template <int RT>
-struct TileSmem {
-    static constexpr int RK = RT < 2 ? 1 : RT / 2;       // steps of 16 ranks
-    static constexpr int LDR = RK * 16 + 8;
-    static constexpr int LDP = RT * 8 + 4;
-    union {
-        struct {
-            __half x[STAGES][TM][LDK], a[STAGES][RT * 8][LDK];
-        } in;
-        __half b[2][NT][LDR];
-    };
-    __half hi[TM][LDR], lo[TM][LDR];
-    float part[TM][LDP];
-    float back[TM];                          // 2^-e of each token
-    int ids[TM];
-};
+// The workspace: per tile of 16 tokens and MMA step the four registers of every lane, hi then lo; then 2^-e of
+// every token.
+template <int PR>
+constexpr int mma_steps() { return PR < 4 ? 1 : PR / 2; }
 
-template <typename T, int RT>
-__global__ void __launch_bounds__(256, RT <= 8 ? 2 : 1) lora_tile_kernel(const LoraArgs p) {
-    using Smem = TileSmem<RT>;
-    constexpr int RK = Smem::RK;
+// PR: pieces of 8 ranks (R <= 8 PR)
+template <int PR>
+__global__ void __launch_bounds__(SW * 32) lora_sums_kernel(const LoraArgs p) {
+    constexpr int LDP = PR * 8 + 1;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-    cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = cluster.num_blocks(), me = cluster.block_rank();
-    const int m0 = blockIdx.x / ctas * TM;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-    if (tid < TM) sm.ids[tid] = m0 + tid < p.M ? adapter_of(p, m0 + tid) : -1;
-    __syncthreads();
+    float (*part)[TM][LDP] = reinterpret_cast<float (*)[TM][LDP]>(smem_raw);      // [SW]
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the second launch's y and B
+    const int m0 = blockIdx.x * TM;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int row = lane & 15;
+    const int id = m0 + row < p.M ? adapter_of(p, m0 + row) : -1;
+    const int id_of[2] = {__shfl_sync(0xffffffffu, id, g), __shfl_sync(0xffffffffu, id, g + 8)};
 
-    // ---- part[m][r] = sum over this CTA's k of x[m, k] A[r, k]; a warp takes 16 tokens and half of each stage
-    const int steps = (p.K + KT - 1) / KT;
-    const int s0 = static_cast<int64_t>(steps) * me / ctas, s1 = static_cast<int64_t>(steps) * (me + 1) / ctas;
-    const int mw = (warp & 3) * 16, kh = warp >> 2, g = lane >> 2, q = lane & 3;
-    const __half* X = reinterpret_cast<const __half*>(p.x);
-    for (int a = next_adapter(sm.ids, -1); a != INT_MAX; a = next_adapter(sm.ids, a)) {
-        const __half* A = reinterpret_cast<const __half*>(p.A) + static_cast<int64_t>(a) * p.R * p.K;
-        const auto stage = [&](int step) {
-            if (step < s1) {
-                const int k0 = step * KT, b = (step - s0) % STAGES;
+    // this warp's part of K, in steps of 32: lane (g, q) holds k 8 q + 0..7 of rows g (and g + 8)
+    const int steps = (p.K + 31) / 32;
+    const int s0 = static_cast<int64_t>(steps) * warp / SW, s1 = static_cast<int64_t>(steps) * (warp + 1) / SW;
+    const int64_t xrow[2] = {static_cast<int64_t>(min(m0 + g, p.M - 1)) * p.K, static_cast<int64_t>(min(m0 + g + 8, p.M - 1)) * p.K};
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    for (int a = next_adapter(id, -1); a != INT_MAX; a = next_adapter(id, a)) {
+        const uint16_t* A = p.A + (static_cast<int64_t>(a) * p.R + g) * p.K;
+        float acc[PR][4];
 #pragma unroll
-                for (int i = tid; i < TM * (KT / 8); i += 256) {
-                    const int r = i >> 3, c = (i & 7) * 8;
-                    const bool live = m0 + r < p.M && k0 + c < p.K;
-                    cp16(&sm.in.x[b][r][c], live ? X + static_cast<int64_t>(m0 + r) * p.K + k0 + c : X, live);
-                }
-                for (int i = tid; i < RT * 8 * (KT / 8); i += 256) {
-                    const int r = i >> 3, c = (i & 7) * 8;
-                    const bool live = r < p.R && k0 + c < p.K;
-                    cp16(&sm.in.a[b][r][c], live ? A + static_cast<int64_t>(r) * p.K + k0 + c : A, live);
-                }
-            }
-            cp_commit();
-        };
-        const bool mine = __any_sync(0xffffffffu, sm.ids[mw + (lane & 15)] == a);
-        float acc[RT][4];
-#pragma unroll
-        for (int n = 0; n < RT; ++n)
+        for (int n = 0; n < PR; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
+        struct Step {
+            uint4 x[2], w[PR];
+        };
+        // every address lies inside (k and the ranks are cut off), so all loads of a step are in flight at once
+        const auto read = [&](int step, Step& f) {
+            const int k = min(step * 32 + 8 * q, p.K - 8);
 #pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) stage(s0 + i);
-        for (int step = s0; step < s1; ++step) {
-            cp_wait<STAGES - 2>();
-            __syncthreads();
-            stage(step + STAGES - 1);
-            const int b = (step - s0) % STAGES;
-            if (mine) {
+            for (int i = 0; i < 2; ++i) f.x[i] = __ldg(reinterpret_cast<const uint4*>(p.x + xrow[i] + k));
 #pragma unroll
-                for (int k = kh * 32; k < kh * 32 + 32; k += 16) {
-                    uint32_t fx[4];
-                    ldsm4(fx, &sm.in.x[b][mw + (lane & 15)][k + (lane >> 4) * 8]);
+            for (int n = 0; n < PR; ++n)
+                f.w[n] = __ldg(reinterpret_cast<const uint4*>(A + static_cast<int64_t>(8 * n < p.R ? 8 * n : 0) * p.K + k));
+        };
+        const auto take = [&](int step, Step& f) {
+            if (step * 32 + 8 * q >= p.K) {  // behind the end: neither operand counts
+                f.x[0] = f.x[1] = none;
 #pragma unroll
-                    for (int n = 0; n < RT; ++n) {
-                        uint32_t fa[2];
-                        ldsm2(fa, &sm.in.a[b][n * 8 + (lane & 7)][k + ((lane >> 3) & 1) * 8]);
-                        mma(acc[n], fx, fa);
-                    }
-                }
+                for (int n = 0; n < PR; ++n) f.w[n] = none;
+            }
+            const uint32_t f0[4] = {f.x[0].x, f.x[1].x, f.x[0].y, f.x[1].y}, f1[4] = {f.x[0].z, f.x[1].z, f.x[0].w, f.x[1].w};
+#pragma unroll
+            for (int n = 0; n < PR; ++n) {
+                const uint32_t b0[2] = {f.w[n].x, f.w[n].y}, b1[2] = {f.w[n].z, f.w[n].w};
+                mma(acc[n], f0, b0);
+                mma(acc[n], f1, b1);
+            }
+        };
+        constexpr int DEEP = PR <= 4 ? 4 : PR <= 8 ? 2 : 1;      // steps in flight
+        Step ring[DEEP];
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i)
+            if (s0 + i < s1) read(s0 + i, ring[i]);
+        for (int step = s0; step < s1; step += DEEP) {
+#pragma unroll
+            for (int i = 0; i < DEEP; ++i) {
+                if (step + i >= s1) break;
+                take(step + i, ring[i]);
+                if (step + i + DEEP < s1) read(step + i + DEEP, ring[i]);
             }
         }
-        cp_wait<0>();
-        // the two halves of the stages are added through shared memory: part is the second's, then the sum
-        const bool own[2] = {sm.ids[mw + g] == a, sm.ids[mw + g + 8] == a};
 #pragma unroll
-        for (int turn = 1; turn >= 0; --turn) {
-            if (kh == turn && mine) {
+        for (int half = 0; half < 2; ++half) {
+            if (id_of[half] != a) continue;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!own[half]) continue;
-#pragma unroll
-                    for (int n = 0; n < RT; ++n) {
-                        float2* at = reinterpret_cast<float2*>(&sm.part[mw + g + 8 * half][n * 8 + 2 * q]);
-                        float2 v = make_float2(acc[n][2 * half], acc[n][2 * half + 1]);
-                        if (turn == 0) {
-                            const float2 o = *at;
-                            v = make_float2(v.x + o.x, v.y + o.y);
-                        }
-                        *at = v;
-                    }
-                }
-            }
-            __syncthreads();                 // and the stages are free for the next adapter
-        }
-    }
-
-    // ---- B of the first tile on its way, then the cluster's sums
-    const int tiles = static_cast<int>((p.N + NT - 1) / NT);
-    const auto fetch = [&](int tile, int a, int buf) {
-        const int rank = rank_of(p, a);
-        const __half* B = reinterpret_cast<const __half*>(p.B) + static_cast<int64_t>(a) * p.N * p.R;
-        const int64_t n0 = static_cast<int64_t>(tile) * NT;
-#pragma unroll 4
-        for (int i = tid; i < NT * RK * 2; i += 256) {
-            const int r = i / (RK * 2), c = (i % (RK * 2)) * 8;
-            const bool live = n0 + r < p.N && c < rank;
-            cp16(&sm.b[buf][r][c], live ? B + (n0 + r) * p.R + c : B, live);
-        }
-        cp_commit();
-    };
-    const int first = next_adapter(sm.ids, -1);
-    if (first != INT_MAX && me < tiles) fetch(me, first, 0);
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-    {                                        // four threads a token
-        const int r = tid >> 2, c0 = (tid & 3) * 4, a = sm.ids[r];
-        const int rank = a >= 0 ? rank_of(p, a) : 0;
-        const float s = a >= 0 && p.scale != nullptr ? p.scale[a] : 1.f;
-        float t[RK][4], top = 0.f;
-#pragma unroll
-        for (int i = 0; i < RK; ++i) {
-            const int c = c0 + 16 * i;
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c < rank) {
-                for (int k = 0; k < ctas; ++k) {
-                    const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&sm.part[r][c], k));
-                    f.x += v.x; f.y += v.y; f.z += v.z; f.w += v.w;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                t[i][j] = c + j < rank ? (&f.x)[j] * s : 0.f;
-                const float mag = fabsf(t[i][j]);
-                top = mag <= FLT_MAX ? fmaxf(top, mag) : top;    // infinities and NaN pass as they are
+            for (int n = 0; n < PR; ++n) {
+                part[warp][g + 8 * half][8 * n + 2 * q] = acc[n][2 * half];
+                part[warp][g + 8 * half][8 * n + 2 * q + 1] = acc[n][2 * half + 1];
             }
         }
-        // no CTA leaves before the others have read its sums
-        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the power of two that brings the largest |t| into [2^14, 2^15)
-        const int ex = static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127;
-        const int e = top > 0.f ? min(14 - ex, 100) : 0;
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        if ((tid & 3) == 0) sm.back[r] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < RK; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float f = t[i][j] * up;
-                const __half h = __float2half_rn(f);
-                sm.hi[r][c0 + 16 * i + j] = h;
-                // an infinite t has no rest
-                sm.lo[r][c0 + 16 * i + j] = __float2half_rn(fabsf(f) <= 65504.f ? f - __half2float(h) : 0.f);
-            }
     }
     __syncthreads();
-
-    // ---- out = epi(y + t B^T); warp: 16 tokens x 64 outputs of a tile.  A thread's columns of a pair of 8-column
-    // products are four neighbours: product column c of product i stands for output 16 (i / 2) + 4 (c / 2) + 2 (i % 2)
-    // + c % 2.
-    const bool wide = (p.N & 3) == 0;
-    const int64_t rows[2] = {m0 + mw + g, m0 + mw + g + 8};
-    const float back[2] = {sm.ids[mw + g] >= 0 ? sm.back[mw + g] : 0.f,
-                           sm.ids[mw + g + 8] >= 0 ? sm.back[mw + g + 8] : 0.f};
-    int buf = 0;
-    for (int tile = me; tile < tiles; tile += ctas) {
-        const int64_t nw = static_cast<int64_t>(tile) * NT + (warp >> 2) * 64 + 4 * q;
-        float acc[4][2][4];                  // [16 outputs][row half][neighbour]: y, then the sum
+    // one warp per token: t in part[0], its scale
+    {
+        const int a = __shfl_sync(0xffffffffu, id, warp);
+        const int rank = a >= 0 ? rank_of(p, a) : 0;
+        const float s = a >= 0 && p.scale != nullptr ? p.scale[a] : 1.f;
+        float top = 0.f;
+        for (int r = lane; r < PR * 8; r += 32) {
+            float t = 0.f;
+            if (r < rank) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-                if (rows[half] < p.M)
-                    get4<T>(p.y, rows[half] * p.N + nw + 16 * i, p.N - nw - 16 * i, wide, acc[i][half]);
-        for (int a = first; a != INT_MAX;) {
-            const int after = next_adapter(sm.ids, a);
-            if (after != INT_MAX) fetch(tile, after, buf ^ 1);
-            else if (tile + ctas < tiles) fetch(tile + ctas, first, buf ^ 1);
-            else cp_commit();
-            cp_wait<1>();
-            __syncthreads();
-            const int rank = rank_of(p, a);
-            if (rank & 7) {                  // columns behind the rank share its last piece: not the adapter's
-                for (int c = rank + tid / NT; c < (rank | 7) + 1; c += 2) sm.b[buf][tid % NT][c] = __float2half_rn(0.f);
-                __syncthreads();
+                for (int w = 0; w < SW; ++w) t += part[w][warp][r];
+                t *= s;
             }
-            if (__any_sync(0xffffffffu, sm.ids[mw + (lane & 15)] == a)) {
-                float c[8][4];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
-#pragma unroll
-                for (int k = 0; k < RK; ++k) {
-                    uint32_t fh[4], fl[4];
-                    ldsm4(fh, &sm.hi[mw + (lane & 15)][k * 16 + (lane >> 4) * 8]);
-                    ldsm4(fl, &sm.lo[mw + (lane & 15)][k * 16 + (lane >> 4) * 8]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int col = lane & 7;
-                        uint32_t fb[2];
-                        ldsm2(fb, &sm.b[buf][(warp >> 2) * 64 + 16 * (i >> 1) + 4 * (col >> 1) + 2 * (i & 1) + (col & 1)]
-                                        [k * 16 + ((lane >> 3) & 1) * 8]);
-                        mma(c[i], fl, fb);
-                        mma(c[i], fh, fb);
-                    }
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (sm.ids[mw + g + 8 * half] != a) continue;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float& f = acc[i >> 1][half][2 * (i & 1) + j];
-                            f = fmaf(c[i][2 * half + j], back[half], f);
-                        }
-                }
-            }
-            __syncthreads();
-            buf ^= 1;
-            a = after;
+            part[0][warp][r] = t;
+            const float mag = fabsf(t);
+            top = mag <= FLT_MAX ? fmaxf(top, mag) : top;        // infinities and NaN pass as they are
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (rows[half] >= p.M) continue;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][half][j] = finish(acc[i][half][j], p.relu_sq);
-                put4<T>(p.out, rows[half] * p.N + nw + 16 * i, p.N - nw - 16 * i, wide, acc[i][half]);
-            }
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int e = scale_of(top);
+        __syncwarp();
+        for (int r = lane; r < PR * 8; r += 32) part[0][warp][r] *= pow2(e);
+        if (lane == 0) {
+            if (m0 + warp < p.M)
+                reinterpret_cast<float*>(p.work + static_cast<int64_t>(gridDim.x) * mma_steps<PR>() * 64)[m0 + warp] = pow2(-e);
+        }
     }
-    cp_wait<0>();
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    __syncthreads();
+    for (int i = threadIdx.x; i < mma_steps<PR>() * 64; i += SW * 32) {
+        const int l = i & 31, lo = (i >> 5) & 1, step = i >> 6, gg = l >> 2, qq = l & 3;
+        uint32_t f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {        // registers: rows gg, gg + 8 of the first two ranks, then of the next
+            const int r = rank_at<PR>(qq, 2 * step + (j >> 1));
+            const float* t = part[0][gg + 8 * (j & 1)];
+            const __half2 v = r < PR * 8 ? __halves2half2(split(t[r], lo), split(t[r + 1], lo)) : __floats2half2_rn(0.f, 0.f);
+            f[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        p.work[(static_cast<int64_t>(blockIdx.x) * mma_steps<PR>() + step) * 64 + lo * 32 + l] = make_uint4(f[0], f[1], f[2], f[3]);
+    }
 }
 
-template <typename T, int RT>
+// out = epi(y + t B^T): a warp takes 16 tokens x 64 outputs.  A lane's columns in a pair of 8-column products are four
+// neighbours: column c of product i stands for output 16 (i / 2) + 4 (c / 2) + 2 (i % 2) + c % 2.
+constexpr int EW = 8;                        // warps of a CTA: 4 tiles of tokens x 2 of outputs, which share B and t in L1
+template <typename T, int PR>
+#ifndef VAR_OCC
+#define VAR_OCC (PR <= 4 ? 3 : 2)
+#endif
+__global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const LoraArgs p) {
+    constexpr int NR = PR, STEPS = mma_steps<PR>();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int tiles = (p.M + TM - 1) / TM, tile = blockIdx.y * 4 + (warp & 3), m0 = tile * TM;
+    if (tile >= tiles) return;
+    const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * 2 + (warp >> 2)) * 64;
+    if (n0 >= p.N) return;
+    const int id = m0 + (lane & 15) < p.M ? adapter_of(p, m0 + (lane & 15)) : -1;
+    const int id_of[2] = {__shfl_sync(0xffffffffu, id, g), __shfl_sync(0xffffffffu, id, g + 8)};
+    const bool wide = (p.N & 3) == 0;
+    const int64_t rows[2] = {m0 + g, m0 + g + 8};
+    float acc[4][2][4];                      // [16 outputs][row half][neighbour]: y, then the sum
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int64_t n = n0 + 16 * i + 4 * q;
+            if (rows[half] < p.M) get4<T>(p.y, rows[half] * p.N + n, p.N - n, wide, acc[i][half]);
+        }
+    bool waited = false;
+    for (int a = next_adapter(id, -1); a != INT_MAX; a = next_adapter(id, a)) {
+        const int rank = rank_of(p, a), rank0 = rank_at<PR>(q, 0);
+        const uint16_t* B = p.B + (static_cast<int64_t>(a) * p.N + n0) * p.R + rank0;
+        const bool ragged = rank < 8 * PR;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {     // 16 outputs
+            uint32_t b[2][NR];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = 16 * (i >> 1) + 4 * (g >> 1) + 2 * h + (g & 1);
+                row_of_b<PR>(B + static_cast<int64_t>(n) * p.R, n0 + n < p.N, rank0, rank, b[h]);
+                if (ragged) {
+#pragma unroll
+                    for (int j = 0; j < NR; ++j) b[h][j] &= keep_of(rank_at<PR>(q, j), rank);
+                }
+            }
+            if (!waited) {                   // y and the first rows of B are on their way; t comes from the launch before
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                waited = true;
+            }
+            float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const uint4* t = p.work + (static_cast<int64_t>(tile) * STEPS + s) * 64 + lane;
+                const uint4 hi = t[0], lo = t[32];
+                const uint32_t fh[4] = {hi.x, hi.y, hi.z, hi.w}, fl[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t fb[2] = {b[h][2 * s < NR ? 2 * s : 0], NR > 1 ? b[h][2 * s + 1 < NR ? 2 * s + 1 : 0] : 0u};
+                    mma(c[h], fl, fb);
+                    mma(c[h], fh, fb);
+                }
+            }
+            const float* back = reinterpret_cast<const float*>(p.work + static_cast<int64_t>(tiles) * STEPS * 64);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (id_of[half] != a) continue;
+                const float f = back[rows[half]];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float& o = acc[i >> 1][half][2 * h + j];
+                        o = fmaf(c[h][2 * half + j], f, o);
+                    }
+            }
+        }
+    }
+    // no CTA ends before the first launch has (its workspace is then free for the next call)
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int64_t n = n0 + 16 * i + 4 * q;
+            if (rows[half] >= p.M) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][half][j] = finish(acc[i][half][j], p.relu_sq);
+            put4<T>(p.out, rows[half] * p.N + n, p.N - n, wide, acc[i][half]);
+        }
+}
+
+template <typename T, int PR>
 cudaError_t launch_tiles(const LoraArgs& a, cudaStream_t s) {
-    constexpr int smem = sizeof(TileSmem<RT>);
-    cudaError_t e = allow_smem<lora_tile_kernel<T, RT>>(smem);
+    constexpr int smem = SW * TM * (PR * 8 + 1) * 4;
+    cudaError_t e = allow_smem<lora_sums_kernel<PR>>(smem);
     if (e != cudaSuccess) return e;
     const int tiles = (a.M + TM - 1) / TM;
+    lora_sums_kernel<PR><<<tiles, SW * 32, smem, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles * CS);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3(static_cast<unsigned>((a.N + 127) / 128), (tiles + 3) / 4);
+    cfg.blockDim = dim3(EW * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CS;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_tile_kernel<T, RT>, a);
+    return cudaLaunchKernelEx(&cfg, lora_outputs_kernel<T, PR>, a);
 }
 
 template <typename T>
@@ -578,7 +585,7 @@ cudaError_t tiles(const LoraArgs& a, cudaStream_t s) {
 bool mis(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 rq_status check_sizes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t R) {
-    if (M < 1 || M >= (1 << 24) || K < 8 || K % 8 != 0 || K > (1 << 30)) return RQ_ERR_SHAPE;
+    if (M < 1 || M > 64 * 65535 || K < 8 || K % 8 != 0 || K > (1 << 30)) return RQ_ERR_SHAPE;
     if (N < 1 || N > (int64_t{1} << 31) - 1 || L < 1 || L > (1 << 30)) return RQ_ERR_SHAPE;
     if (R < 8 || R % 8 != 0 || R > RQ_MAX_LORA_RANK) return RQ_ERR_SHAPE;
     return RQ_OK;
@@ -599,16 +606,24 @@ using namespace rq;
 
 extern "C" {
 
+size_t rq_lora_work_bytes(int64_t M, int64_t R) {
+    if (check_sizes(M, 8, 1, 1, R) != RQ_OK || M <= kLoraTokens) return 0;
+    const int64_t tiles = (M + TM - 1) / TM, steps = R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8;
+    return static_cast<size_t>(tiles * (steps * 64 * sizeof(uint4) + TM * sizeof(float)));
+}
+
 rq_status rq_lora_add(const uint16_t* x, int64_t M, int64_t K, const uint16_t* A, const uint16_t* B, int64_t L,
                       int64_t R, const int32_t* ids, const int32_t* ranks, const float* scale, const void* y,
-                      void* out, int64_t N, int dtype, int epilogue, int* dev_status, rq_stream_t stream) {
+                      void* out, int64_t N, int dtype, int epilogue, void* work, int* dev_status,
+                      rq_stream_t stream) {
     if (dtype != RQ_OUT_F32 && dtype != RQ_OUT_F16) return RQ_ERR_RANGE;
     if (epilogue != RQ_EPI_NONE && epilogue != RQ_EPI_RELU_SQ) return RQ_ERR_RANGE;
     const rq_status st = check_sizes(M, K, N, L, R);
     if (st != RQ_OK) return st;
     if (x == nullptr || A == nullptr || B == nullptr || ids == nullptr || y == nullptr || out == nullptr)
         return RQ_ERR_NULL;
-    if (mis(x, 16) || mis(A, 16) || mis(B, 16) || mis(y, 16) || mis(out, 16) || mis(ids, 4) ||
+    if (work == nullptr && M > kLoraTokens) return RQ_ERR_NULL;
+    if (mis(x, 16) || mis(A, 16) || mis(B, 16) || mis(y, 16) || mis(out, 16) || mis(work, 16) || mis(ids, 4) ||
         mis(ranks, 4) || mis(scale, 4) || mis(dev_status, 4))
         return RQ_ERR_ALIGN;
     LoraArgs a = {};
@@ -620,6 +635,7 @@ rq_status rq_lora_add(const uint16_t* x, int64_t M, int64_t K, const uint16_t* A
     a.scale = scale;
     a.y = y;
     a.out = out;
+    a.work = static_cast<uint4*>(work);
     a.status = dev_status;
     a.N = N;
     a.M = static_cast<int>(M);

@@ -14,6 +14,7 @@ struct LoraArgs {
     const float* scale;                      // [L] or NULL: 1
     const void* y;                           // [M, N]
     void* out;                               // [M, N]
+    uint4* work;                             // many tokens only
     int* status;
     int64_t N;
     int M, K, R, L;

@@ -12,7 +12,7 @@ struct NormArgs {
     const float *post_weight, *post_bias, *pre_weight, *pre_bias, *alpha;   // [D] or NULL
     int64_t ld_y, ld_add, ld_gate, M;
     int D, post, post_group, pre, gate_act;  // post_group 0: the whole row
-    float eps_post, eps_pre;
+    float eps_post, eps_pre, inv_row, inv_group;     // 1 / D, 1 / post_group
 };
 
 cudaError_t launch_norm_residual(const NormArgs& a, bool half, cudaStream_t s);

@@ -81,7 +81,9 @@ def lib():
     L.rq_gemv_p8_g16.restype = i32
     L.rq_gemv_p4a_g32.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp]
     L.rq_gemv_p4a_g32.restype = i32
-    L.rq_lora_add.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, i64, i32, i32, vp, vp]
+    L.rq_lora_work_bytes.argtypes = [i64, i64]
+    L.rq_lora_work_bytes.restype = ctypes.c_size_t
+    L.rq_lora_add.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, i64, i32, i32, vp, vp, vp]
     L.rq_lora_add.restype = i32
     f32 = ctypes.c_float
     L.rq_norm_residual.argtypes = [vp, i64, i64, i64, i32, i32, i64, vp, vp, f32, vp, i64, vp, i64, i32, vp, vp, i32,
@@ -403,8 +405,10 @@ def lora_add(x, A, B, ids, y, out=None, ranks=None, scale=None, epilogue: int = 
         _on_gpu(c, at)
     if out is None:
         out = torch.empty_like(y)
+    work = None if M <= MAX_DECODE_M else torch.empty(lib().rq_lora_work_bytes(M, R), dtype=torch.uint8, device=x.device)
     st = lib().rq_lora_add(x.data_ptr(), M, K, A.data_ptr(), B.data_ptr(), L, R, ids.data_ptr(), _p(ranks), _p(scale),
-                           y.data_ptr(), out.data_ptr(), N, _REAL[dtype], epilogue, _p(dev_status), _stream_of(at))
+                           y.data_ptr(), out.data_ptr(), N, _REAL[dtype], epilogue, _p(work), _p(dev_status),
+                           _stream_of(at))
     if st != OK:
         raise RQError(st, c)
     return out
