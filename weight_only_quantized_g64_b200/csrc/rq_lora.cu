@@ -487,6 +487,9 @@ __global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const Lo
         const int rank = rank_of(p, a), rank0 = rank_at<PR>(q, 0);
         const uint16_t* B = p.B + (static_cast<int64_t>(a) * p.N + n0) * p.R + rank0;
         const bool ragged = rank < 8 * PR;
+        constexpr bool HOLD = PR <= 8;       // t stays in registers; else it is read for every 16 outputs
+        uint4 held[HOLD ? STEPS : 1][2];
+        const uint4* work = p.work + static_cast<int64_t>(tile) * STEPS * 64 + lane;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {     // 16 outputs
             uint32_t b[2][NR];
@@ -503,11 +506,17 @@ __global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const Lo
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 waited = true;
             }
+            if (HOLD && i == 0) {
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    held[HOLD ? s : 0][0] = work[s * 64];
+                    held[HOLD ? s : 0][1] = work[s * 64 + 32];
+                }
+            }
             float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                const uint4* t = p.work + (static_cast<int64_t>(tile) * STEPS + s) * 64 + lane;
-                const uint4 hi = t[0], lo = t[32];
+                const uint4 hi = HOLD ? held[HOLD ? s : 0][0] : work[s * 64], lo = HOLD ? held[HOLD ? s : 0][1] : work[s * 64 + 32];
                 const uint32_t fh[4] = {hi.x, hi.y, hi.z, hi.w}, fl[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {

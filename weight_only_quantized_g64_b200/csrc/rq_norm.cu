@@ -94,108 +94,131 @@ __device__ __forceinline__ float sum(uint64_t p) {
     return f.x + f.y;
 }
 
-constexpr int MAX_WARPS = 32;
+constexpr int MAX_WARPS = 16;
 
-// The mean (0 for the rms norm) and 1 / sqrt(mean square + eps) of the 1 / inv_n
-// values that `width` consecutive lanes (a power of two) or, width 0, the whole
-// CTA hold.  v: V pieces, the first `pieces` of them real, the others zeros.
-template <int V>
-__device__ __forceinline__ void stats(const Piece* v, int pieces, bool layer, int width, float eps, float inv_n,
-                                      Moments* shared, float& mean, float& rstd) {
-    Moments a = {8.f * pieces, 0.f, 0.f};
-    if (layer && pieces > 0) {
-        uint64_t s = add2(add2(v[0].v[0], v[0].v[1]), add2(v[0].v[2], v[0].v[3]));
+// For R rows of which a thread holds V pieces each (the first `pieces` real, the
+// others zeros): the mean (0 for the rms norm) and 1 / sqrt(mean square + eps) of
+// the 1 / inv_n values of a row that `width` consecutive lanes (a power of two)
+// or, width 0, the whole CTA hold.
+template <int R, int V, bool LAYER>
+__device__ __forceinline__ void stats(const Piece (&v)[R][V], int pieces, int width, float eps, float inv_n,
+                                      Moments (*shared)[MAX_WARPS], float (&mean)[R], float (&rstd)[R]) {
+    Moments a[R];
 #pragma unroll
-        for (int i = 1; i < V; ++i)
+    for (int r = 0; r < R; ++r) {
+        a[r] = {8.f * pieces, 0.f, 0.f};
+        if (LAYER) {
+            uint64_t s = add2(add2(v[r][0].v[0], v[r][0].v[1]), add2(v[r][0].v[2], v[r][0].v[3]));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s = add2(s, v[i].v[j]);
-        a.mean = V == 1 ? sum(s) * 0.125f : __fdividef(sum(s), a.n);
-    }
-    if (pieces > 0) {
-        const uint64_t away = both(-a.mean);
+            for (int i = 1; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s = add2(s, v[r][i].v[j]);
+            a[r].mean = V == 1 ? sum(s) * 0.125f : pieces > 0 ? __fdividef(sum(s), a[r].n) : 0.f;
+        }
+        const uint64_t away = both(-a[r].mean);
         uint64_t s = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (V == 1 || i < pieces) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint64_t d = layer ? add2(v[i].v[j], away) : v[i].v[j];
+                    const uint64_t d = LAYER ? add2(v[r][i].v[j], away) : v[r][i].v[j];
                     s = fma2(d, d, s);
                 }
             }
-        a.m2 = sum(s);
+        a[r].m2 = sum(s);
     }
-    if (width) {
-        for (int m = 1; m < width; m <<= 1) {
-            if (layer) a = join_xor(a, m);
-            else a.m2 += __shfl_xor_sync(0xffffffffu, a.m2, m);
+    const auto join_lanes = [&](int m) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (LAYER) a[r] = join_xor(a[r], m);
+            else a[r].m2 += __shfl_xor_sync(0xffffffffu, a[r].m2, m);
         }
+    };
+    if (width) {
+        for (int m = 1; m < width; m <<= 1) join_lanes(m);
     } else {
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) join_lanes(m);
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-        if (layer) {
+        if (lane == 0) {
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1) a = join_xor(a, m);
-            if (lane == 0) shared[warp] = a;
-        } else {
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) a.m2 += __shfl_xor_sync(0xffffffffu, a.m2, m);
-            if (lane == 0) shared[warp].m2 = a.m2;
+            for (int r = 0; r < R; ++r) {
+                if (LAYER) shared[r][warp] = a[r];
+                else shared[r][warp].m2 = a[r].m2;
+            }
         }
         __syncthreads();
-        // the first 16 lanes (a CTA of 1024 threads: all) join the warps' parts, whatever their number
-        if (layer) {
-            a = lane < warps ? shared[lane] : Moments{0.f, 0.f, 0.f};
+        // 16 lanes join the warps' parts, whatever their number (at most 16)
 #pragma unroll
-            for (int m = 1; m < 16; m <<= 1) a = join_xor(a, m);
-            if (warps > 16) a = join_xor(a, 16);
-            a.mean = __shfl_sync(0xffffffffu, a.mean, 0);
-        } else {
-            a.m2 = lane < warps ? shared[lane].m2 : 0.f;
-#pragma unroll
-            for (int m = 1; m < 16; m <<= 1) a.m2 += __shfl_xor_sync(0xffffffffu, a.m2, m);
-            if (warps > 16) a.m2 += __shfl_xor_sync(0xffffffffu, a.m2, 16);
+        for (int r = 0; r < R; ++r) {
+            const int w = lane & 15;
+            if (LAYER) a[r] = w < warps ? shared[r][w] : Moments{0.f, 0.f, 0.f};
+            else a[r].m2 = w < warps ? shared[r][w].m2 : 0.f;
         }
-        a.m2 = __shfl_sync(0xffffffffu, a.m2, 0);
+#pragma unroll
+        for (int m = 1; m < 16; m <<= 1) join_lanes(m);
     }
-    mean = a.mean;
-    rstd = rsqrtf(a.m2 * inv_n + eps);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        mean[r] = a[r].mean;
+        rstd[r] = rsqrtf(fmaf(a[r].m2, inv_n, eps));
+    }
 }
 
-__device__ __forceinline__ void apply(Piece& v, const NormArgs& p, bool post, int c, float mean, float rstd) {
-    const float* w = post ? p.post_weight : p.pre_weight;
-    const float* b = post ? p.post_bias : p.pre_bias;
-    if ((post ? p.post : p.pre) == RQ_NORM_LAYER) {
-        const uint64_t away = both(-mean);
+// v = (v - mean) * rstd * weight + bias
+template <int R, int V, bool LAYER>
+__device__ __forceinline__ void normed_as(Piece (&u)[R][V], int pieces, int group, float eps, float inv_n,
+                                          const float* weight, const float* bias, Moments (*shared)[MAX_WARPS]) {
+    float mean[R], rstd[R];
+    const int threads = blockDim.x;
+    const auto apply = [&](Piece& v, float m, float s) {
+        if (LAYER) {
+            const uint64_t away = both(-m);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v.v[j] = add2(v.v[j], away);
+            for (int j = 0; j < 4; ++j) v.v[j] = add2(v.v[j], away);
+        }
+        const uint64_t r = both(s);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v.v[j] = mul2(v.v[j], r);
+    };
+    if (group == 0) stats<R, V, LAYER>(u, pieces, 0, eps, inv_n, shared, mean, rstd);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (group != 0) {                    // group / 8 neighbouring threads hold a group
+            Piece one[R][1];
+#pragma unroll
+            for (int r = 0; r < R; ++r) one[r][0] = u[r][i];
+            stats<R, 1, LAYER>(one, i < pieces, group / 8, eps, inv_n, nullptr, mean, rstd);
+        }
+        if (i >= pieces) continue;
+        const int c = (threadIdx.x + i * threads) * 8;
+#pragma unroll
+        for (int r = 0; r < R; ++r) apply(u[r][i], mean[r], rstd[r]);
+        if (weight != nullptr) {
+            const Piece w = load<float>(weight, c);
+#pragma unroll
+            for (int r = 0; r < R; ++r) times(u[r][i], w);
+        }
+        if (bias != nullptr) {
+            const Piece b = load<float>(bias, c);
+#pragma unroll
+            for (int r = 0; r < R; ++r) plus(u[r][i], b);
+        }
     }
-    const uint64_t r = both(rstd);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v.v[j] = mul2(v.v[j], r);
-    if (w != nullptr) times(v, load<float>(w, c));
-    if (b != nullptr) plus(v, load<float>(b, c));
 }
 
-template <int V>
-__device__ __forceinline__ void normed(Piece* u, int pieces, const NormArgs& p, bool post, int threads,
-                                       Moments* shared) {
+template <int R, int V>
+__device__ __forceinline__ void normed(Piece (&u)[R][V], int pieces, const NormArgs& p, bool post,
+                                       Moments (*shared)[MAX_WARPS]) {
     const int kind = post ? p.post : p.pre;
     if (kind == RQ_NORM_NONE) return;
-    const bool layer = kind == RQ_NORM_LAYER;
-    const float eps = post ? p.eps_post : p.eps_pre;
-    float mean, rstd;
-    if (!post || p.post_group == 0) {
-        stats<V>(u, pieces, layer, 0, eps, p.inv_row, shared, mean, rstd);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < pieces) apply(u[i], p, post, (threadIdx.x + i * threads) * 8, mean, rstd);
-    } else {                                 // post_group / 8 neighbouring threads hold a group
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            stats<1>(&u[i], i < pieces, layer, p.post_group / 8, eps, p.inv_group, nullptr, mean, rstd);
-            if (i < pieces) apply(u[i], p, post, (threadIdx.x + i * threads) * 8, mean, rstd);
-        }
-    }
+    const int group = post ? p.post_group : 0;
+    const float eps = post ? p.eps_post : p.eps_pre, inv_n = group ? p.inv_group : p.inv_row;
+    const float* w = post ? p.post_weight : p.pre_weight;
+    const float* b = post ? p.post_bias : p.pre_bias;
+    if (kind == RQ_NORM_LAYER) normed_as<R, V, true>(u, pieces, group, eps, inv_n, w, b, shared);
+    else normed_as<R, V, false>(u, pieces, group, eps, inv_n, w, b, shared);
 }
 
 // Relative error below 2^-20: the hardware's 2^x and 1/x are good to 2^-22 and
@@ -210,21 +233,34 @@ __device__ __forceinline__ uint64_t sigmoid2(uint64_t x) {
     return pack2(t.x, t.y);
 }
 
-// u = (u + add) * act(gate), h' = h + alpha u of the piece at channel c; take() gives
-// the next of the tensors that are there.
-template <typename Take>
-__device__ __forceinline__ void combine(Piece& u, const NormArgs& p, int c, Take&& take) {
-    if (p.add != nullptr) plus(u, take(p.add, p.ld_add));
-    if (p.gate != nullptr) {
-        const Piece g = take(p.gate, p.ld_gate);
-        if (p.gate_act != RQ_GATE_SIGMOID) times(u, g);
-        if (p.gate_act != RQ_GATE_IDENTITY) {
+// u = (u + add) * act(gate), h' = h + alpha u of the pieces of R rows at channel c;
+// take(r) gives the next of the tensors that are there.
+template <int R, typename Take>
+__device__ __forceinline__ void combine(Piece* (&u)[R], const NormArgs& p, int c, Take&& take) {
+    if (p.add != nullptr) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], sigmoid2(g.v[j]));
+        for (int r = 0; r < R; ++r) plus(*u[r], take(r, p.add, p.ld_add));
+    }
+    if (p.gate != nullptr) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const Piece g = take(r, p.gate, p.ld_gate);
+            if (p.gate_act != RQ_GATE_SIGMOID) times(*u[r], g);
+            if (p.gate_act != RQ_GATE_IDENTITY) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) u[r]->v[j] = mul2(u[r]->v[j], sigmoid2(g.v[j]));
+            }
         }
     }
-    if (p.alpha != nullptr) times(u, load<float>(p.alpha, c));
-    if (p.h != nullptr) plus(u, take(p.h, p.D));
+    if (p.alpha != nullptr) {
+        const Piece f = load<float>(p.alpha, c);
+#pragma unroll
+        for (int r = 0; r < R; ++r) times(*u[r], f);
+    }
+    if (p.h != nullptr) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) plus(*u[r], take(r, p.h, p.D));
+    }
 }
 
 __device__ __forceinline__ void cp16(void* dst, const void* src) {
@@ -234,63 +270,78 @@ __device__ __forceinline__ void cp16(void* dst, const void* src) {
                  : "memory");
 }
 
-// Rows of up to 4096 channels: row blockIdx.x, + gridDim.x, ...; one piece per thread.
-constexpr int RING = 3;                      // rows on their way, the current one among them
-template <typename T>
+// Rows of up to 4096 channels: R rows at a time, one piece of each per thread,
+// the next R (with R = 1 the next two) on their way.  Two rows at a time share
+// the loads of the weights, the tests of what is there and the barriers.
+template <typename T, int R>
 __global__ void __launch_bounds__(512, 2) norm_rows_kernel(const NormArgs p) {
     constexpr int PB = 8 * sizeof(T);        // bytes of a piece
+    constexpr int RING = R == 1 ? 3 : 2;
     extern __shared__ __align__(16) unsigned char ring[];
-    __shared__ Moments shared[2][2][MAX_WARPS];      // of alternate rows: one norm alone has one barrier a row
+    __shared__ Moments shared[2][2][R][MAX_WARPS];   // of alternate rows: one norm alone has one barrier a row
     const int threads = blockDim.x, tid = threadIdx.x, c = tid * 8;
     const bool in = c < p.D;
     const int tensors = 1 + (p.add != nullptr) + (p.gate != nullptr) + (p.h != nullptr);
-    const int tensor_bytes = threads * PB, row_bytes = tensors * tensor_bytes;
+    const int piece_step = threads * PB;
     unsigned char* mine = ring + tid * PB;
-    // where this thread's pieces of the next row to be fetched lie
-    const auto start = [&](const void* base, int64_t ld) {
-        return static_cast<const char*>(base) + (blockIdx.x * ld + c) * static_cast<int64_t>(sizeof(T));
-    };
-    const char *py = start(p.y, p.ld_y), *pa = start(p.add, p.ld_add), *pg = start(p.gate, p.ld_gate),
-               *ph = start(p.h, p.D);
-    const int64_t step = gridDim.x * static_cast<int64_t>(sizeof(T));
-    const auto fetch = [&](int64_t row, int slot) {
-        if (row < p.M && in) {
-            unsigned char* to = mine + slot * row_bytes;
-            const auto one = [&](const char*& from, int64_t ld) {
+    const auto fetch = [&](int64_t row, int slot) {          // R rows from this one on
+        if (in) {
+            unsigned char* to = mine + slot * tensors * R * piece_step;
+            const auto one = [&](const void* base, int64_t ld) {
+                const char* from = static_cast<const char*>(base) + (row * ld + c) * static_cast<int64_t>(sizeof(T));
 #pragma unroll
-                for (int i = 0; i < PB; i += 16) cp16(to + i, from + i);
-                to += tensor_bytes;
-                from += ld * step;
+                for (int r = 0; r < R; ++r) {
+                    if (row + r < p.M) {
+#pragma unroll
+                        for (int j = 0; j < PB; j += 16) cp16(to + j, from + j);
+                    }
+                    to += piece_step;
+                    from += ld * static_cast<int64_t>(sizeof(T));
+                }
             };
-            one(py, p.ld_y);
-            if (p.add != nullptr) one(pa, p.ld_add);
-            if (p.gate != nullptr) one(pg, p.ld_gate);
-            if (p.h != nullptr) one(ph, p.D);
+            one(p.y, p.ld_y);
+            if (p.add != nullptr) one(p.add, p.ld_add);
+            if (p.gate != nullptr) one(p.gate, p.ld_gate);
+            if (p.h != nullptr) one(p.h, p.D);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * R;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * R;
 #pragma unroll
-    for (int i = 0; i < RING - 1; ++i) fetch(blockIdx.x + static_cast<int64_t>(i) * gridDim.x, i);
+    for (int i = 0; i < RING - 1; ++i) fetch(row + i * stride, i);
     int slot = 0, parity = 0;
-    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-        fetch(row + static_cast<int64_t>(RING - 1) * gridDim.x, slot == 0 ? RING - 1 : slot - 1);
+    for (; row < p.M; row += stride) {
+        fetch(row + (RING - 1) * stride, slot == 0 ? RING - 1 : slot - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
-        Piece u[1] = {};
-        const unsigned char* from = mine + slot * row_bytes;
-        const auto take = [&](const void*, int64_t) {
-            const uint4* q = reinterpret_cast<const uint4*>(from);
-            from += tensor_bytes;
+        Piece u[R][1] = {};
+        const unsigned char* const from = mine + slot * tensors * R * piece_step;
+        const auto take = [&](int place) {
+            const uint4* q = reinterpret_cast<const uint4*>(from + place * piece_step);
             return expand<T>(q[0], sizeof(T) == 4 ? q[1] : make_uint4(0u, 0u, 0u, 0u));
         };
-        if (in) u[0] = take(nullptr, 0);
-        normed<1>(u, in, p, true, threads, shared[parity][0]);
         if (in) {
-            combine(u[0], p, c, take);
-            if (p.h_out != nullptr) store<T>(p.h_out, row * p.D + c, u[0]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) u[r][0] = take(r);   // (a row behind the last: whatever the slot holds)
+        }
+        normed<R, 1>(u, in, p, true, shared[parity][0]);
+        if (in) {
+            int place = R;
+            Piece* rows[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) rows[r] = &u[r][0];
+            combine<R>(rows, p, c, [&](int, const void*, int64_t) { return take(place++); });
+            if (p.h_out != nullptr) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (row + r < p.M) store<T>(p.h_out, (row + r) * p.D + c, u[r][0]);
+            }
         }
         if (p.x != nullptr) {
-            normed<1>(u, in, p, false, threads, shared[parity][1]);
-            if (in) store<__half>(p.x, row * p.D + c, u[0]);
+            normed<R, 1>(u, in, p, false, shared[parity][1]);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (in && row + r < p.M) store<__half>(p.x, (row + r) * p.D + c, u[r][0]);
         }
         slot = slot == RING - 1 ? 0 : slot + 1;
         parity ^= 1;
@@ -300,48 +351,54 @@ __global__ void __launch_bounds__(512, 2) norm_rows_kernel(const NormArgs p) {
 
 // Longer rows: a CTA each, V pieces per thread.
 template <typename T, int V>
-__global__ void __launch_bounds__(1024) norm_row_kernel(const NormArgs p) {
-    __shared__ Moments shared[2][MAX_WARPS];
+__global__ void __launch_bounds__(512) norm_row_kernel(const NormArgs p) {
+    __shared__ Moments shared[2][1][MAX_WARPS];
     const int64_t row = blockIdx.x;
     const int threads = blockDim.x, all = p.D / 8;
     int pieces = 0;                          // threadIdx.x + i * threads < D / 8
 #pragma unroll
     for (int i = 0; i < V; ++i) pieces += static_cast<int>(threadIdx.x) + i * threads < all;
-    Piece u[V] = {};
+    Piece u[1][V] = {};
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        if (i < pieces) u[i] = load<T>(p.y, row * p.ld_y + (threadIdx.x + i * threads) * 8);
-    normed<V>(u, pieces, p, true, threads, shared[0]);
+        if (i < pieces) u[0][i] = load<T>(p.y, row * p.ld_y + (threadIdx.x + i * threads) * 8);
+    normed<1, V>(u, pieces, p, true, shared[0]);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (i >= pieces) break;
         const int c = (threadIdx.x + i * threads) * 8;
-        combine(u[i], p, c, [&](const void* base, int64_t ld) { return load<T>(base, row * ld + c); });
-        if (p.h_out != nullptr) store<T>(p.h_out, row * p.D + c, u[i]);
+        Piece* rows[1] = {&u[0][i]};
+        combine<1>(rows, p, c, [&](int, const void* base, int64_t ld) { return load<T>(base, row * ld + c); });
+        if (p.h_out != nullptr) store<T>(p.h_out, row * p.D + c, u[0][i]);
     }
     if (p.x == nullptr) return;
-    normed<V>(u, pieces, p, false, threads, shared[1]);
+    normed<1, V>(u, pieces, p, false, shared[1]);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        if (i < pieces) store<__half>(p.x, row * p.D + (threadIdx.x + i * threads) * 8, u[i]);
+        if (i < pieces) store<__half>(p.x, row * p.D + (threadIdx.x + i * threads) * 8, u[0][i]);
+}
+
+template <typename T, int R>
+cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
+    constexpr int RING = R == 1 ? 3 : 2;
+    const int threads = (a.D / 8 + 31) / 32 * 32;
+    const int tensors = 1 + (a.add != nullptr) + (a.gate != nullptr) + (a.h != nullptr);
+    const int row_bytes = threads * 8 * static_cast<int>(sizeof(T));
+    const int smem = RING * R * tensors * row_bytes;
+    if (smem > (200 << 10)) return launch_rows<T, 1>(a, s);              // two fp32 rows of four tensors
+    const cudaError_t e = allow_smem<norm_rows_kernel<T, R>>(200 << 10);
+    if (e != cudaSuccess) return e;
+    const int per_sm = std::max(1, std::min(std::min(1024 / threads, 32), (220 << 10) / (smem + 3072)));
+    const int64_t grid = std::min<int64_t>((a.M + R - 1) / R, static_cast<int64_t>(num_sms()) * per_sm);
+    norm_rows_kernel<T, R><<<static_cast<unsigned>(grid), threads, smem, s>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch(const NormArgs& a, cudaStream_t s) {
     const int pieces = a.D / 8;
-    if (pieces <= 512) {
-        const int threads = (pieces + 31) / 32 * 32;
-        const int tensors = 1 + (a.add != nullptr) + (a.gate != nullptr) + (a.h != nullptr);
-        const int smem = RING * tensors * threads * 8 * static_cast<int>(sizeof(T));   // at most 192 KB
-        const cudaError_t e = allow_smem<norm_rows_kernel<T>>(RING * 4 * 512 * 8 * static_cast<int>(sizeof(T)));
-        if (e != cudaSuccess) return e;
-        // CTAs that an SM holds: 1024 threads at 64 registers, and their rings
-        const int per_sm = std::max(1, std::min(1024 / threads, (220 << 10) / (smem + 2048)));
-        const int64_t grid = std::min<int64_t>(a.M, static_cast<int64_t>(num_sms()) * per_sm);
-        norm_rows_kernel<T><<<static_cast<unsigned>(grid), threads, smem, s>>>(a);
-        return cudaGetLastError();
-    }
-    norm_row_kernel<T, 2><<<static_cast<unsigned>(a.M), ((pieces + 1) / 2 + 31) / 32 * 32, 0, s>>>(a);
+    if (pieces <= 512) return a.M <= 4 * num_sms() ? launch_rows<T, 1>(a, s) : launch_rows<T, 2>(a, s);
+    norm_row_kernel<T, 4><<<static_cast<unsigned>(a.M), ((pieces + 3) / 4 + 31) / 32 * 32, 0, s>>>(a);
     return cudaGetLastError();
 }
 
