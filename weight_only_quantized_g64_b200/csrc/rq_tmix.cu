@@ -1,304 +1,658 @@
 // rq_tmix.cu -- the time-mix recurrence over sequences (and, run backwards,
 // the gradient of its state) and over single tokens.
 //
-// Sequences: every row of the 64 x 64 state is its own recurrence, so the
-// rows are spread over lanes and stay in registers for the whole sequence:
-// four lanes share a row (16 keys each), a lane holds RPL rows.  Per token a
-// lane reads its 16 keys of five vectors from shared memory once for all its
-// rows; the dot products finish with two shuffles.  Four producer warps load
-// and convert the next chunk of tokens (the decay costs an exponential and a
-// sigmoid per channel) while the others run through the current one.
-// What bounds it: 5 * 64 * 64 fp32 FMA per token and head (packed in pairs),
-// and for few heads the chain of one dot product and its shuffles per token.
+// Sequences, forwards.  Tokens are taken in chunks of C = 16.  With the decay
+// divided out inside a chunk (W_t = prod_{s <= t} w_s; R_t = W_t r_t, A_t =
+// W_{t-1} a_t, B_t = b_t / W_t, K_t = k_t / W_t as rows of 16 x 64 matrices; w >
+// 0.545, so 1 / W <= 1.7e4), L keeping t >= s and M keeping t > s of a 16 x 16
+// matrix, and T = (1 - M(A B^T))^-1, the chunk maps the state S before it to
+//   Y = R' S^T + M' V,     S <- (S + (S A'^T) B + V^T K') diag(W_last)
+//   A' = T A,  R' = R + L(R B^T) A',  N = T M(A K^T),
+//   K' = K + N^T B,  M' = L(R K^T) + L(R B^T) N:
+// matrix products only, and the rows of S still do not meet.  Four warps hold 16
+// rows of S each, in the registers of the tensor cores' accumulators, which are
+// also their first operand once the summed index is taken in the order 2q, 2q+1
+// instead of q, q+4.  Three groups of four warps prepare A', R', B, K', M' of the
+// chunks ahead in turn (with the same products): one chunk's preparation is a
+// chain of small dependent steps, three times as long as its use.
 //
-// The backward direction is the same walk with other roles: with G the
-// gradient of the state,
-//   G <- G + dy_t r_t^T;   G <- G diag(w_t) + (G b_t) a_t^T      (t descending)
-// and G is stored behind each chunk of kTmixChunk tokens.
+// fp32 on the tensor cores: every operand is split into two tf32 parts (22 bits
+// of it), and lo*hi + hi*lo + hi*hi go into the fp32 accumulator; what is lost
+// is about 2^-22 of each product.  fp16 values are one part, exactly.  On this
+// GPU an SM retires 512 such multiplications a cycle, 171 of them useful: about
+// 204 + 87 MMAs per warp and chunk, 8 cycles each, bound the kernel (plain fp32
+// FMAs would be 128 a cycle, and spent their time on shuffles and on reading
+// each token's vectors for every row: 1.16 ms where this takes VAR_MS ms, 8192
+// tokens of 64 heads, the longest sequence 58 % of them).
+//
+// The products see every token of a chunk at once, so a value that is not finite
+// would reach earlier tokens through a factor of 0.  A chunk with one in r, d, k,
+// a or b, which reach every row, is therefore taken token by token, as the
+// formula is written; one in v leaves the products, and makes its row NaN from
+// its token on.
+//
+// Backwards: with G the gradient of the state behind a chunk, times W_last,
+//   G <- G + (G B'^T) A + dY^T R',   B' = T^T B,
+// and G is stored behind each chunk.
 #include "rq_tmix.cuh"
 
 namespace rq {
 namespace {
 
-constexpr int CT = kTmixChunk;               // tokens staged at once
-constexpr int NPW = 4;                       // producer warps: one piece of each vector per thread
-static_assert(NPW * 32 == CT * kHead / 8);
-// vectors staged per token: decay - 1, then forward k, a, b, r; backward r, b, a
-constexpr int nvec(bool rev) { return rev ? 4 : 5; }
+constexpr int C = kTmixChunk;
+constexpr int LA = kHead + 8;                // rows read 8 bytes at a time along the keys: 8 banks apart
+constexpr int LB = kHead + 4;                // rows read in pairs of tokens: 2 rows 8 banks apart
+constexpr int LS = C + 8;
+constexpr int GROUPS = 3, BUFFERS = 2;       // preparing groups, and chunks that each may have ready
+static_assert(C == 16 && kHead == 64);
+// 16-byte accesses: every row, and so every array, is a multiple of 16 bytes
+static_assert(LA % 4 == 0 && LB % 4 == 0 && LS % 4 == 0 && kHead % 8 == 0);
 
-template <int ROWS, bool REV>
-struct Stage {
-    float vec[nvec(REV)][CT][kHead];
-    float row[CT][ROWS];                     // v, or dy
+// What the row warps need of a chunk.  Forwards / backwards: A' / B', R' / -, B /
+// A, K' / R', M' / -, v / dy.
+template <typename T, bool REV>
+struct alignas(16) Chunk {
+    float a[C][LA];
+    float r[REV ? 1 : C][LA];
+    float b[C][LB], k[C][LB];
+    float m[REV ? 1 : C][LS];
+    float last[kHead];                       // W of the last token
+    T v[C][kHead + 8];
+    int bad;                                 // a value of the chunk is not finite
 };
-template <int ROWS, bool REV>
-struct Smem {
-    Stage<ROWS, REV> st[2];
-    float y[REV ? 1 : 2][REV ? 1 : CT][ROWS];
+template <typename T, bool REV>
+struct alignas(16) Group {
+    Chunk<T, REV> ch[BUFFERS];
+    float x[C][LA], R[C][LA];                // the chunk in preparation: A / B, R
+    float y[REV ? C : 1][LB];                // - / A'
+    float abt[C][LS], rb[C][LS], t[C][LS];   // M(A B^T) transposed, L(R B^T), T
+    float ak[REV ? 1 : C][LS], rk[REV ? 1 : C][LS], n[REV ? 1 : C][LS];
+};
+template <typename T, bool REV>
+struct alignas(16) Smem {
+    Group<T, REV> group[GROUPS];
+    float y[REV ? 1 : 4][C][C + 4];          // of each row warp
 };
 
-// The producers' part of a chunk: tokens [t0, t0 + nt) of head h, from global
-// memory into registers (one piece of 8 elements of each vector per thread) ...
-template <typename T, int ROWS, bool REV>
-struct Raw {
-    Raw8 vec[nvec(REV)], row;
+// x = hi + lo: hi rounded to 11 bits, lo the rest, which the MMA cuts to 11 bits.
+// Bit operations: the conversions to tf32 run at a fraction of their rate.  (A
+// NaN may lose itself in hi, and is then in lo.)
+struct Two {
+    uint32_t hi, lo;
 };
-template <typename T, int ROWS, bool REV>
-__device__ __forceinline__ void load_chunk(const TmixArgs& p, Raw<T, ROWS, REV>& raw, int64_t t0, int nt, int h,
-                                           int row0, int pt) {
-    // in[]: r, d, k, v, a, b.  Order of the staged vectors (source indices):
-    constexpr int src[5] = {1, REV ? 0 : 2, REV ? 5 : 4, REV ? 4 : 5, 0};
-    const int t = pt >> 3, c = (pt & 7) * 8;
-    const int64_t head = static_cast<int64_t>(h) * kHead;
-    if (t < nt) {
+__device__ __forceinline__ Two split(float x) {
+    const uint32_t hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    return {hi, __float_as_uint(x - __uint_as_float(hi))};
+}
+// {hi, hi, lo, lo} of two values
+__device__ __forceinline__ float4 quad(float x, float y) {
+    const Two a = split(x), b = split(y);
+    return make_float4(__uint_as_float(a.hi), __uint_as_float(b.hi), __uint_as_float(a.lo), __uint_as_float(b.lo));
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The first operand of one step (8 of the summed index) in two parts: rows g and
+// g + 8, and of each the elements 2q and 2q + 1 of the step.
+struct Rows {
+    uint32_t hi[4], lo[4];
+};
+__device__ __forceinline__ Rows rows_of(float g0, float g1, float h0, float h1) {
+    Rows r;
+    const Two a = split(g0), b = split(h0), c = split(g1), d = split(h1);
+    r.hi[0] = a.hi; r.hi[1] = b.hi; r.hi[2] = c.hi; r.hi[3] = d.hi;
+    r.lo[0] = a.lo; r.lo[1] = b.lo; r.lo[2] = c.lo; r.lo[3] = d.lo;
+    return r;
+}
+// N products of one step: the second operands are elements 2q and 2q + 1 of the
+// step, column g, as quads.  One part after the other over all N, as an MMA waits
+// 21 cycles for the one before it on the same sum.  EXACT: the first operand is
+// its hi part.
+template <int N, bool EXACT = false>
+__device__ __forceinline__ void products(float (*c)[4], const Rows& a, const float4 (&b)[N]) {
+    if (!EXACT) {
 #pragma unroll
-        for (int v = 0; v < nvec(REV); ++v)
-            raw.vec[v] = load8(static_cast<const T*>(p.in[src[v]]) + (t0 + t) * p.ld + head + c);
+        for (int n = 0; n < N; ++n) mma(c[n], a.lo, __float_as_uint(b[n].x), __float_as_uint(b[n].y));
     }
-    const int rt = pt / (ROWS / 8), rc = (pt % (ROWS / 8)) * 8;
-    if (rt < nt) {
-        const T* rows = REV ? static_cast<const T*>(p.dy) + (t0 + rt) * p.H * kHead
-                            : static_cast<const T*>(p.in[3]) + (t0 + rt) * p.ld;
-        raw.row = load8(rows + head + row0 + rc);
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma(c[n], a.hi, __float_as_uint(b[n].z), __float_as_uint(b[n].w));
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma(c[n], a.hi, __float_as_uint(b[n].x), __float_as_uint(b[n].y));
+}
+__device__ __forceinline__ float4 quad_at(const float* p) { return *reinterpret_cast<const float4*>(p); }
+// Second operands from a matrix whose rows are the columns of the product (two
+// neighbours of a row), and from one whose rows are the summed index (two rows).
+__device__ __forceinline__ float4 along(const float* p) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    return quad(f.x, f.y);
+}
+__device__ __forceinline__ float4 down(const float* p, int ld) { return quad(p[0], p[ld]); }
+template <int LD>
+__device__ __forceinline__ Rows rows_at(const float (*m)[LD], int g, int k) {     // rows g, g + 8; elements k, k + 1
+    const float2 x = *reinterpret_cast<const float2*>(&m[g][k]), y = *reinterpret_cast<const float2*>(&m[g + 8][k]);
+    return rows_of(x.x, x.y, y.x, y.y);
+}
+template <int LD>
+__device__ __forceinline__ Rows columns_at(const float (*m)[LD], int g, int k) {  // of the transposed matrix
+    return rows_of(m[k][g], m[k + 1][g], m[k][g + 8], m[k + 1][g + 8]);
+}
+__device__ __forceinline__ void zero(float (&c)[4]) { c[0] = c[1] = c[2] = c[3] = 0.f; }
+
+// Named barriers: 1 + group: its own steps; then for each group and buffer one
+// that says "ready" and one that says "free".  Each is used by 128 threads that
+// arrive and 128 that wait, once a turn.
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
+__device__ __forceinline__ bool group_any(int group, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(p ? 1u : 0u), "r"(1 + group)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ int ready_id(int c) { return 1 + GROUPS + (c % GROUPS) * BUFFERS + c / GROUPS % BUFFERS; }
+__device__ __forceinline__ int free_id(int c) { return ready_id(c) + GROUPS * BUFFERS; }
+static_assert(1 + GROUPS + 2 * GROUPS * BUFFERS <= 16);
+__device__ __forceinline__ void arrive_at(int id) { asm volatile("barrier.cta.arrive %0, 256;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void wait_at(int id) { asm volatile("barrier.cta.sync %0, 256;" ::"r"(id) : "memory"); }
+
+// ---------------------------------------------------- the preparing warps --
+// Thread: 8 channels of one token, the tokens 4 w .. 4 w + 3 in warp w.
+struct Raw {
+    Raw8 in[6];                              // r, d, k, v (or dy), a, b
+};
+template <typename T, bool REV>
+__device__ __forceinline__ void load_chunk(const TmixArgs& p, Raw& raw, int64_t t0, int nt, int h, int pt) {
+    const int t = pt >> 3;
+    if (t >= nt) return;
+    const int64_t head = static_cast<int64_t>(h) * kHead + (pt & 7) * 8, at = (t0 + t) * p.ld + head;
+#pragma unroll
+    for (int v = 0; v < 6; ++v) {
+        if (REV && v == 2) continue;
+        if (REV && v == 3) raw.in[v] = load8(static_cast<const T*>(p.dy) + (t0 + t) * p.H * kHead + head);
+        else raw.in[v] = load8(static_cast<const T*>(p.in[v]) + at);
     }
 }
-// ... and, converted, from there into a stage.
-template <typename T, int ROWS, bool REV>
-__device__ __forceinline__ void stage_chunk(Stage<ROWS, REV>& st, const Raw<T, ROWS, REV>& raw, int nt, int pt) {
-    const int t = pt >> 3, c = (pt & 7) * 8;
-    const auto put = [](float* to, const float* f) {
+
+template <typename T, bool REV, typename Next>
+__device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, int group, const Raw& raw, int nt, int pt,
+                                        Next&& next) {
+    const int warp = pt >> 5, lane = pt & 31, g = lane >> 2, q = lane & 3;
+    const int token = pt >> 3, k0 = (pt & 7) * 8;
+    float r[8], w[8], k[8], a[8], b[8];
+    bool bad = false;
+    {
+        // a token behind the last changes nothing: zeros, and a decay of 1
+        const bool in = token < nt;
+        const auto take = [&](int v, float* f) {
+            if (in) {
+                cvt8<T>(raw.in[v], f);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = 0.f;
+            }
+        };
+        uint4* to = reinterpret_cast<uint4*>(&ch.v[token][k0]);
+        to[0] = in ? raw.in[3].u[0] : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (sizeof(T) == 4) to[1] = in ? raw.in[3].u[1] : make_uint4(0u, 0u, 0u, 0u);
+        take(0, r);
+        take(1, w);
+        if (!REV) take(2, k);
+        take(4, a);
+        take(5, b);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sum += (fabsf(r[j]) + fabsf(a[j])) + (fabsf(b[j]) + (REV ? 0.f : fabsf(k[j])));
+            bad |= w[j] != w[j];
+            w[j] = in ? decay_m1(w[j]) : 0.f;
+        }
+        bad |= !(sum < 1e30f);               // (and none so large that its product with 1 / W is not finite)
+        next();                              // the inputs of the chunk after this one, into raw
+    }
+    if constexpr (!REV) {
+        bad = group_any(group, bad);
+        if (pt == 0) ch.bad = bad;
+        if (bad) {                           // the inputs themselves, for the formula
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ch.a[token][k0 + j] = a[j];
+                ch.r[token][k0 + j] = r[j];
+                ch.b[token][k0 + j] = b[j];
+                ch.k[token][k0 + j] = k[j];
+            }
+            return;
+        }
+    }
+    // W: products over the tokens, in the warp and then of the warps before
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        w[j] += 1.f;
+        float o = __shfl_up_sync(0xffffffffu, w[j], 8);
+        w[j] *= lane >= 8 ? o : 1.f;
+        o = __shfl_up_sync(0xffffffffu, w[j], 16);
+        w[j] *= lane >= 16 ? o : 1.f;
+    }
+    const auto put8 = [](float* to, const float* f) {
         reinterpret_cast<float4*>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
         reinterpret_cast<float4*>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
     };
-    float f[8];
-    if (t < nt) {
+    float (*parts)[kHead] = reinterpret_cast<float (*)[kHead]>(&sm.t[0][0]);     // (t comes later)
+    static_assert(sizeof(sm.t) >= 4 * kHead * sizeof(float));
+    if (lane >= 24) put8(&parts[warp][k0], w);
+    group_sync(group);
+    float before[8];
 #pragma unroll
-        for (int v = 0; v < nvec(REV); ++v) {
-            cvt8<T>(raw.vec[v], f);
-            if (v == 0) {
+    for (int j = 0; j < 8; ++j) before[j] = 1.f;
+    for (int i = 0; i < warp; ++i) {
+        const float4 x = quad_at(&parts[i][k0]), y = quad_at(&parts[i][k0 + 4]);
+        before[0] *= x.x; before[1] *= x.y; before[2] *= x.z; before[3] *= x.w;
+        before[4] *= y.x; before[5] *= y.y; before[6] *= y.z; before[7] *= y.w;
+    }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = decay_m1(f[j]);
+    for (int j = 0; j < 8; ++j) {
+        const float up = __shfl_up_sync(0xffffffffu, w[j], 8);
+        const float prev = before[j] * (lane >= 8 ? up : 1.f);
+        w[j] *= before[j];
+        float back;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(back) : "f"(w[j]));
+        r[j] *= w[j];
+        a[j] *= prev;
+        b[j] *= back;
+        if (!REV) k[j] *= back;
+    }
+    put8(&sm.R[token][k0], r);
+    put8(REV ? &ch.b[token][k0] : &sm.x[token][k0], a);
+    put8(REV ? &sm.x[token][k0] : &ch.b[token][k0], b);
+    if (!REV) put8(&ch.k[token][k0], k);
+    if (token == C - 1) put8(&ch.last[k0], w);
+    group_sync(group);
+
+    // the 16 x 16 products, one per warp
+    if (!REV || warp < 2) {
+        const bool second = REV ? warp == 1 : warp >= 2;         // R, else A
+        const float* x = second ? &sm.R[0][0] : REV ? &ch.b[0][0] : &sm.x[0][0];
+        const int lx = second || !REV ? LA : LB;
+        const float* z = REV ? &sm.x[0][0] : warp & 1 ? &ch.k[0][0] : &ch.b[0][0];
+        const int lz = REV ? LA : LB;
+        float c[4][4];                       // two column halves, each as two sums
+#pragma unroll
+        for (int n = 0; n < 4; ++n) zero(c[n]);
+#pragma unroll 2
+        for (int k = 0; k < kHead; k += 16) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float* row = x + g * lx + k + 8 * i + 2 * q;
+                const float2 u = *reinterpret_cast<const float2*>(row), v = *reinterpret_cast<const float2*>(row + 8 * lx);
+                const float* col = z + g * lz + k + 8 * i + 2 * q;
+                const float4 b[2] = {along(col), along(col + 8 * lz)};
+                products<2>(c + 2 * i, rows_of(u.x, u.y, v.x, v.y), b);
             }
-            put(&st.vec[v][t][c], f);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[n][j] += c[n + 2][j];
+        const int what = REV ? 2 * warp : warp;              // 0: A B^T, 1: A K^T, 2: R B^T, 3: R K^T
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = g + 8 * (j >> 1), s = 8 * n + 2 * q + (j & 1);
+                const float v = t > s || (t == s && what >= 2) ? c[n][j] : 0.f;
+                if (what == 0) sm.abt[s][t] = v;
+                if (what == 2) sm.rb[t][s] = v;
+                if constexpr (!REV) {
+                    if (what == 1) sm.ak[t][s] = v;
+                    if (what == 3) sm.rk[t][s] = v;
+                }
+            }
+    }
+    group_sync(group);
+
+    // T (lanes 0..15: its columns) and N = T M(A K^T) (lanes 16..31), solved from the first row down
+    if (warp == 0) {
+        const int c = lane & 15;
+        float x[C];
+#pragma unroll
+        for (int t = 0; t < C; ++t) {
+            x[t] = t == c ? 1.f : 0.f;
+            if constexpr (!REV) x[t] = lane < 16 ? x[t] : sm.ak[t][c];
+        }
+#pragma unroll
+        for (int s = 0; s < C - 1; ++s) {
+#pragma unroll
+            for (int t4 = (s + 1) / 4 * 4; t4 < C; t4 += 4) {
+                const float4 m = *reinterpret_cast<const float4*>(&sm.abt[s][t4]);
+                x[t4] = fmaf(m.x, x[s], x[t4]);              // (zeros up to s: those are done)
+                x[t4 + 1] = fmaf(m.y, x[s], x[t4 + 1]);
+                x[t4 + 2] = fmaf(m.z, x[s], x[t4 + 2]);
+                x[t4 + 3] = fmaf(m.w, x[s], x[t4 + 3]);
+            }
+        }
+        if (lane < 16) {
+#pragma unroll
+            for (int t = 0; t < C; ++t) sm.t[t][c] = x[t];
+        } else if constexpr (!REV) {
+#pragma unroll
+            for (int t = 0; t < C; ++t) sm.n[t][c] = x[t];
         }
     }
-    const int rt = pt / (ROWS / 8), rc = (pt % (ROWS / 8)) * 8;
-    if (rt < nt) {
-        cvt8<T>(raw.row, f);
-        put(&st.row[rt][rc], f);
+    group_sync(group);
+
+    // 16 keys per warp, in two products of 8 columns
+    const int kw = warp * 16;
+    float c[2][4];
+    const auto put = [&](float* to, int ld) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float* at = to + g * ld + kw + 8 * n + 2 * q;
+            *reinterpret_cast<float2*>(at) = make_float2(c[n][0], c[n][1]);
+            *reinterpret_cast<float2*>(at + 8 * ld) = make_float2(c[n][2], c[n][3]);
+        }
+    };
+    const auto take = [&](const float* from, int ld) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const float* at = from + g * ld + kw + 8 * n + 2 * q;
+            const float2 x = *reinterpret_cast<const float2*>(at), y = *reinterpret_cast<const float2*>(at + 8 * ld);
+            c[n][0] = x.x; c[n][1] = x.y; c[n][2] = y.x; c[n][3] = y.y;
+        }
+    };
+    // c += m z, or with the columns of m, z the rows of 16 tokens
+    const auto multiply = [&](const float (*m)[LS], bool columns, const float* z, int ld) {
+#pragma unroll
+        for (int s = 0; s < C; s += 8) {
+            const float* at = z + (s + 2 * q) * ld + kw + g;
+            const float4 b[2] = {down(at, ld), down(at + 8, ld)};
+            products<2>(c, columns ? columns_at(m, g, s + 2 * q) : rows_at(m, g, s + 2 * q), b);
+        }
+    };
+    zero(c[0]);
+    zero(c[1]);
+    if constexpr (!REV) {
+        multiply(sm.t, false, &sm.x[0][0], LA);                  // A' = T A
+        put(&ch.a[0][0], LA);
+        take(&ch.k[0][0], LB);                                   // K' = K + N^T B
+        multiply(sm.n, true, &ch.b[0][0], LB);
+        put(&ch.k[0][0], LB);
+        __syncwarp();
+        take(&sm.R[0][0], LA);                                   // R' = R + L(R B^T) A'
+        multiply(sm.rb, false, &ch.a[0][0], LA);
+        put(&ch.r[0][0], LA);
+        if (warp < 2) {                                          // M' = L(R K^T) + L(R B^T) N, 8 columns each
+            float e[1][4];
+            const float* at = &sm.rk[g][8 * warp + 2 * q];
+            const float2 x = *reinterpret_cast<const float2*>(at), y = *reinterpret_cast<const float2*>(at + 8 * LS);
+            e[0][0] = x.x; e[0][1] = x.y; e[0][2] = y.x; e[0][3] = y.y;
+#pragma unroll
+            for (int s = 0; s < C; s += 8) {
+                const float4 b[1] = {down(&sm.n[s + 2 * q][8 * warp + g], LS)};
+                products<1>(e, rows_at(sm.rb, g, s + 2 * q), b);
+            }
+            *reinterpret_cast<float2*>(&ch.m[g][8 * warp + 2 * q]) = make_float2(e[0][0], e[0][1]);
+            *reinterpret_cast<float2*>(&ch.m[g + 8][8 * warp + 2 * q]) = make_float2(e[0][2], e[0][3]);
+        }
+    } else {
+        multiply(sm.t, false, &ch.b[0][0], LB);                  // A' = T A
+        put(&sm.y[0][0], LB);
+        zero(c[0]);                                              // B' = T^T B
+        zero(c[1]);
+        multiply(sm.t, true, &sm.x[0][0], LA);
+        put(&ch.a[0][0], LA);
+        __syncwarp();
+        take(&sm.R[0][0], LA);                                   // R' = R + L(R B^T) A'
+        multiply(sm.rb, false, &sm.y[0][0], LB);
+        put(&ch.k[0][0], LB);
     }
 }
 
-template <typename T, int ROWS>
-__device__ __forceinline__ void store_y(const TmixArgs& p, const float (*y)[ROWS], int64_t t0, int nt, int h,
-                                        int row0, int pt) {
-    T* out = static_cast<T*>(p.out[0]);
-    for (int piece = pt; piece < nt * (ROWS / 4); piece += NPW * 32) {
-        const int t = piece / (ROWS / 4), c = (piece % (ROWS / 4)) * 4;
-        store4(out + ((t0 + t) * p.H + h) * kHead + row0 + c, *reinterpret_cast<const float4*>(&y[t][c]));
+// --------------------------------------------------------- the row warps --
+// S[n][j]: row g (j < 2) or g + 8, key 8 n + 2 q + j % 2
+using State = float[8][4];
+
+template <typename T>
+__device__ __forceinline__ void forward_chunk(State& S, const Chunk<T, false>& ch, float (*y)[C + 4], int row, int lane) {
+    const int g = lane >> 2, q = lane & 3;
+    float XY[4][4];
+    float (*X)[4] = XY, (*Y)[4] = XY + 2;
+    int from[2] = {C, C};                    // first token of the row whose v is not finite
+#pragma unroll
+    for (int n = 0; n < 4; ++n) zero(XY[n]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {            // X = S A'^T, Y = S R'^T
+        const float4 b[4] = {along(&ch.a[g][8 * k + 2 * q]), along(&ch.a[8 + g][8 * k + 2 * q]),
+                             along(&ch.r[g][8 * k + 2 * q]), along(&ch.r[8 + g][8 * k + 2 * q])};
+        products<4>(XY, rows_of(S[k][0], S[k][1], S[k][2], S[k][3]), b);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {            // + V^T M'^T; S += X B + V^T K'
+        const Rows x = rows_of(X[s][0], X[s][1], X[s][2], X[s][3]);
+        const T *v0 = &ch.v[8 * s + 2 * q][row + g], *v1 = v0 + kHead + 8;
+        float vf[4] = {to_f32(v0[0]), to_f32(v1[0]), to_f32(v0[8]), to_f32(v1[8])};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (!(fabsf(vf[j]) < 1e30f)) {
+                vf[j] = 0.f;
+                from[j >> 1] = min(from[j >> 1], 8 * s + 2 * q + (j & 1));
+            }
+        const Rows v = rows_of(vf[0], vf[1], vf[2], vf[3]);
+        constexpr bool EXACT = sizeof(T) == 2;
+        const float4 m[2] = {along(&ch.m[g][8 * s + 2 * q]), along(&ch.m[8 + g][8 * s + 2 * q])};
+        products<2, EXACT>(Y, v, m);
+#pragma unroll
+        for (int n = 0; n < 8; n += 4) {
+            float4 b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = down(&ch.b[8 * s + 2 * q][8 * (n + i) + g], LB);
+            products<4>(S + n, x, b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = down(&ch.k[8 * s + 2 * q][8 * (n + i) + g], LB);
+            products<4, EXACT>(S + n, v, b);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const float2 w = *reinterpret_cast<const float2*>(&ch.last[8 * n + 2 * q]);
+        S[n][0] *= w.x;
+        S[n][1] *= w.y;
+        S[n][2] *= w.x;
+        S[n][3] *= w.y;
+    }
+    if (__any_sync(0xffffffffu, min(from[0], from[1]) < C)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            from[i] = min(from[i], __shfl_xor_sync(0xffffffffu, from[i], 1));
+            from[i] = min(from[i], __shfl_xor_sync(0xffffffffu, from[i], 2));
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (from[i] < C) S[n][2 * i + j] = NAN;
+                    if (n < 2 && 8 * n + 2 * q + j >= from[i]) Y[n & 1][2 * i + j] = NAN;
+                }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[8 * n + 2 * q + (j & 1)][g + 8 * (j >> 1)] = Y[n][j];
+}
+
+// The formula as it is written, for chunks with values that are not finite.
+template <typename T>
+__device__ __forceinline__ void forward_tokens(State& S, const Chunk<T, false>& ch, const T* d, int64_t ld,
+                                               float (*y)[C + 4], int row, int lane, int nt) {
+    const int g = lane >> 2, q = lane & 3;
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+        const float *r = ch.r[t], *a = ch.a[t], *b = ch.b[t], *k = ch.k[t];
+        float u[2] = {0.f, 0.f}, out[2] = {0.f, 0.f};
+        const T* dt = d + t * ld;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j >> 1] = fmaf(S[n][j], a[8 * n + 2 * q + (j & 1)], u[j >> 1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            u[i] += __shfl_xor_sync(0xffffffffu, u[i], 1);
+            u[i] += __shfl_xor_sync(0xffffffffu, u[i], 2);
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const float m[2] = {decay_m1(to_f32(dt[8 * n + 2 * q])), decay_m1(to_f32(dt[8 * n + 2 * q + 1]))};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = 8 * n + 2 * q + (j & 1), i = j >> 1;
+                S[n][j] = fmaf(S[n][j], m[j & 1], S[n][j]);
+                S[n][j] = fmaf(to_f32(ch.v[t][row + g + 8 * i]), k[key], S[n][j]);
+                S[n][j] = fmaf(u[i], b[key], S[n][j]);
+                out[i] = fmaf(S[n][j], r[key], out[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            out[i] += __shfl_xor_sync(0xffffffffu, out[i], 1);
+            out[i] += __shfl_xor_sync(0xffffffffu, out[i], 2);
+            if (q == 0) y[t][g + 8 * i] = out[i];
+        }
     }
 }
 
-// One CTA: NCW compute warps of 8 RPL rows each, of one head of one sequence.
-template <typename T, int RPL, int NCW, bool REV>
-__global__ void __launch_bounds__((NCW + NPW) * 32) tmix_scan_kernel(const TmixArgs p) {
-    constexpr int ROWS = NCW * 8 * RPL, SPLIT = kHead / ROWS;
+template <typename T>
+__device__ __forceinline__ void backward_chunk(State& G, const Chunk<T, true>& ch, int row, int lane) {
+    const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const float2 w = *reinterpret_cast<const float2*>(&ch.last[8 * n + 2 * q]);
+        G[n][0] *= w.x;
+        G[n][1] *= w.y;
+        G[n][2] *= w.x;
+        G[n][3] *= w.y;
+    }
+    float X[4][4];                           // as two sums
+#pragma unroll
+    for (int n = 0; n < 4; ++n) zero(X[n]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {            // X = G B'^T
+        const float4 b[2] = {along(&ch.a[g][8 * k + 2 * q]), along(&ch.a[8 + g][8 * k + 2 * q])};
+        products<2>(X + (k & 1 ? 2 : 0), rows_of(G[k][0], G[k][1], G[k][2], G[k][3]), b);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) X[n][j] += X[n + 2][j];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {            // G += X A + dY^T R'
+        const Rows x = rows_of(X[s][0], X[s][1], X[s][2], X[s][3]);
+        const T *v0 = &ch.v[8 * s + 2 * q][row + g], *v1 = v0 + kHead + 8;
+        const Rows v = rows_of(to_f32(v0[0]), to_f32(v1[0]), to_f32(v0[8]), to_f32(v1[8]));
+#pragma unroll
+        for (int n = 0; n < 8; n += 4) {
+            float4 b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = down(&ch.b[8 * s + 2 * q][8 * (n + i) + g], LB);
+            products<4>(G + n, x, b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = down(&ch.k[8 * s + 2 * q][8 * (n + i) + g], LB);
+            products<4, sizeof(T) == 2>(G + n, v, b);
+        }
+    }
+}
+
+// One CTA: one head of one sequence; warps 0..3 hold its rows, the others prepare.
+template <typename T, bool REV>
+__global__ void __launch_bounds__(128 * (1 + GROUPS), 1) tmix_scan_kernel(const TmixArgs p) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    Smem<ROWS, REV>& sm = *reinterpret_cast<Smem<ROWS, REV>*>(smem_raw);
-
-    const int part = blockIdx.x % SPLIT;
-    const int h = (blockIdx.x / SPLIT) % p.H;
-    const int seq = blockIdx.x / SPLIT / p.H;
-    const int row0 = part * ROWS;
+    Smem<T, REV>& sm = *reinterpret_cast<Smem<T, REV>*>(smem_raw);
+    const int h = blockIdx.x % p.H, seq = blockIdx.x / p.H;
     int lo, hi;
     if (!sequence_of(p, seq, lo, hi)) return;
     const int64_t slot = state_of(p, seq);
-    const int nchunk = (hi - lo + CT - 1) / CT;
+    const int chunks = (hi - lo + C - 1) / C;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const auto chunk_of = [&](int c) { return REV ? nchunk - 1 - c : c; };
-    const auto tokens_in = [&](int c) { return min(CT, hi - lo - c * CT); };
+    const auto chunk_of = [&](int c) { return REV ? chunks - 1 - c : c; };
+    const auto start_of = [&](int c) { return lo + static_cast<int64_t>(chunk_of(c)) * C; };
+    const auto tokens_in = [&](int c) { return min(C, hi - lo - chunk_of(c) * C); };
 
-    if (warp >= NCW) {                       // producers
-        // a chunk's loads are issued one chunk ahead of its conversion
-        const int pt = threadIdx.x - NCW * 32;
-        Raw<T, ROWS, REV> raw;
+    if (warp >= 4) {
+        const int group = (warp - 4) / 4, pt = threadIdx.x & 127;
+        Group<T, REV>& mine = sm.group[group];
+        Raw raw;
         const auto load = [&](int c) {
-            if (c < nchunk)
-                load_chunk<T, ROWS, REV>(p, raw, lo + static_cast<int64_t>(chunk_of(c)) * CT, tokens_in(chunk_of(c)),
-                                         h, row0, pt);
+            if (c < chunks) load_chunk<T, REV>(p, raw, start_of(c), tokens_in(c), h, pt);
         };
-        const auto stage = [&](int c) {
-            if (c < nchunk) stage_chunk<T, ROWS, REV>(sm.st[c & 1], raw, tokens_in(chunk_of(c)), pt);
-        };
-        load(0);
-        stage(0);
-        load(1);
-        __syncthreads();
-        for (int c = 0; c < nchunk; ++c) {
-            stage(c + 1);
-            load(c + 2);
-            if constexpr (!REV) {
-                if (c > 0) store_y<T, ROWS>(p, sm.y[(c - 1) & 1], lo + static_cast<int64_t>(c - 1) * CT, CT, h,
-                                            row0, pt);
-            }
-            __syncthreads();
-        }
-        if constexpr (!REV) {
-            if (nchunk > 0) store_y<T, ROWS>(p, sm.y[(nchunk - 1) & 1], lo + static_cast<int64_t>(nchunk - 1) * CT,
-                                             tokens_in(nchunk - 1), h, row0, pt);
+        load(group);
+        for (int c = group; c < chunks; c += GROUPS) {
+            if (c >= GROUPS * BUFFERS) wait_at(free_id(c));
+            prepare<T, REV>(mine, mine.ch[c / GROUPS % BUFFERS], group, raw, tokens_in(c), pt, [&] { load(c + GROUPS); });
+            arrive_at(ready_id(c));
         }
         return;
     }
 
-    // compute warps: lane (g, q) holds rows wrow .. wrow + RPL - 1, keys 16 i + 4 q + 0..3
-    const int q = lane & 3, wrow = (warp * 8 + (lane >> 2)) * RPL;
-    uint64_t S[RPL][8];
+    const int g = lane >> 2, q = lane & 3, row = 16 * warp;
     const int64_t head_state = (slot * p.H + h) * kHead * kHead;
+    const auto place = [&](int n, int i) { return (row + g + 8 * i) * kHead + 8 * n + 2 * q; };
+    State S;
 #pragma unroll
-    for (int r = 0; r < RPL; ++r) {
+    for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p.state_in != nullptr && slot >= 0)
-                f = *reinterpret_cast<const float4*>(p.state_in + head_state + (row0 + wrow + r) * kHead + 16 * i +
-                                                     4 * q);
-            S[r][2 * i] = pack2(f.x, f.y);
-            S[r][2 * i + 1] = pack2(f.z, f.w);
+        for (int i = 0; i < 2; ++i) {
+            float2 f = make_float2(0.f, 0.f);
+            if (p.state_in != nullptr && slot >= 0) f = *reinterpret_cast<const float2*>(p.state_in + head_state + place(n, i));
+            S[n][2 * i] = f.x;
+            S[n][2 * i + 1] = f.y;
         }
-    }
-    float* const ck = REV ? p.gckpt : p.ckpt;
-    const auto store_state = [&](float* dst) {
+    const auto store_state = [&](float* to) {
 #pragma unroll
-        for (int r = 0; r < RPL; ++r) {
+        for (int n = 0; n < 8; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 a = unpack2(S[r][2 * i]), b = unpack2(S[r][2 * i + 1]);
-                *reinterpret_cast<float4*>(dst + (row0 + wrow + r) * kHead + 16 * i + 4 * q) =
-                    make_float4(a.x, a.y, b.x, b.y);
-            }
-        }
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<float2*>(to + place(n, i)) = make_float2(S[n][2 * i], S[n][2 * i + 1]);
     };
-    __syncthreads();
-    for (int c = 0; c < nchunk; ++c) {
-        const int ch = chunk_of(c), nt = tokens_in(ch);
-        if (ck != nullptr) store_state(ck + ((ckpt_base(lo, seq) + ch) * p.H + h) * kHead * kHead);
-        const Stage<ROWS, REV>& st = sm.st[c & 1];
-#pragma unroll 2
-        for (int s = 0; s < nt; ++s) {
-            const int t = REV ? nt - 1 - s : s;
-            const auto vec = [&](int v, int i) {
-                return *reinterpret_cast<const ulonglong2*>(&st.vec[v][t][16 * i + 4 * q]);
-            };
-            float row[RPL];
-#pragma unroll
-            for (int r = 0; r < RPL; ++r) row[r] = st.row[t][wrow + r];
-            if constexpr (REV) {             // G += dy r^T before the dot product
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const ulonglong2 x = vec(1, i);
-#pragma unroll
-                    for (int r = 0; r < RPL; ++r) {
-                        const uint64_t rr = pack2(row[r], row[r]);
-                        S[r][2 * i] = fma2(rr, x.x, S[r][2 * i]);
-                        S[r][2 * i + 1] = fma2(rr, x.y, S[r][2 * i + 1]);
-                    }
-                }
-            }
-            // q = S a (backward: G b)
-            float dot[RPL];
-            {
-                uint64_t acc[RPL][2];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const ulonglong2 x = vec(2, i);
-#pragma unroll
-                    for (int r = 0; r < RPL; ++r) {
-                        acc[r][0] = i ? fma2(S[r][2 * i], x.x, acc[r][0]) : mul2(S[r][0], x.x);
-                        acc[r][1] = i ? fma2(S[r][2 * i + 1], x.y, acc[r][1]) : mul2(S[r][1], x.y);
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < RPL; ++r) {
-                    const float2 f = unpack2(add2(acc[r][0], acc[r][1]));
-                    dot[r] = f.x + f.y;
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < RPL; ++r) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], 1);
-#pragma unroll
-            for (int r = 0; r < RPL; ++r) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], 2);
-            // S = S + (w - 1) S (+ v k^T), then + q b^T
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const ulonglong2 w = vec(0, i);
-#pragma unroll
-                for (int r = 0; r < RPL; ++r) {
-                    S[r][2 * i] = fma2(S[r][2 * i], w.x, S[r][2 * i]);
-                    S[r][2 * i + 1] = fma2(S[r][2 * i + 1], w.y, S[r][2 * i + 1]);
-                }
-                if constexpr (!REV) {
-                    const ulonglong2 x = vec(1, i);
-#pragma unroll
-                    for (int r = 0; r < RPL; ++r) {
-                        const uint64_t rr = pack2(row[r], row[r]);
-                        S[r][2 * i] = fma2(rr, x.x, S[r][2 * i]);
-                        S[r][2 * i + 1] = fma2(rr, x.y, S[r][2 * i + 1]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const ulonglong2 x = vec(3, i);
-#pragma unroll
-                for (int r = 0; r < RPL; ++r) {
-                    const uint64_t dd = pack2(dot[r], dot[r]);
-                    S[r][2 * i] = fma2(dd, x.x, S[r][2 * i]);
-                    S[r][2 * i + 1] = fma2(dd, x.y, S[r][2 * i + 1]);
-                }
-            }
-            if constexpr (!REV) {            // y = S r
-                uint64_t acc[RPL][2];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const ulonglong2 x = vec(4, i);
-#pragma unroll
-                    for (int r = 0; r < RPL; ++r) {
-                        acc[r][0] = i ? fma2(S[r][2 * i], x.x, acc[r][0]) : mul2(S[r][0], x.x);
-                        acc[r][1] = i ? fma2(S[r][2 * i + 1], x.y, acc[r][1]) : mul2(S[r][1], x.y);
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < RPL; ++r) {
-                    const float2 f = unpack2(add2(acc[r][0], acc[r][1]));
-                    float y = f.x + f.y;
-                    y += __shfl_xor_sync(0xffffffffu, y, 1);
-                    y += __shfl_xor_sync(0xffffffffu, y, 2);
-                    if (q == 0) sm.y[c & 1][t][wrow + r] = y;
-                }
-            }
+    float* const ck = REV ? p.gckpt : p.ckpt;
+    for (int c = 0; c < chunks; ++c) {
+        if (ck != nullptr) store_state(ck + ((ckpt_base(lo, seq) + chunk_of(c)) * p.H + h) * kHead * kHead);
+        const Chunk<T, REV>& ch = sm.group[c % GROUPS].ch[c / GROUPS % BUFFERS];
+        wait_at(ready_id(c));
+        if constexpr (REV) {
+            backward_chunk<T>(S, ch, row, lane);
+        } else {
+            if (ch.bad)
+                forward_tokens<T>(S, ch, static_cast<const T*>(p.in[1]) + start_of(c) * p.ld + static_cast<int64_t>(h) * kHead,
+                                  p.ld, sm.y[warp], row, lane, tokens_in(c));
+            else forward_chunk<T>(S, ch, sm.y[warp], row, lane);
         }
-        __syncthreads();
+        if (c + GROUPS * BUFFERS < chunks) arrive_at(free_id(c));        // (as often as it is waited for)
+        if constexpr (!REV) {
+            __syncwarp();
+            const int t = lane >> 1, r = 8 * (lane & 1);
+            if (t < tokens_in(c)) {
+                T* to = static_cast<T*>(p.out[0]) + ((start_of(c) + t) * p.H + h) * kHead + row + r;
+                store4(to, *reinterpret_cast<const float4*>(&sm.y[warp][t][r]));
+                store4(to + 4, *reinterpret_cast<const float4*>(&sm.y[warp][t][r + 4]));
+            }
+            __syncwarp();
+        }
     }
     if (p.state_out != nullptr && slot >= 0) store_state(p.state_out + head_state);
 }
 
-template <typename T, int RPL, int NCW, bool REV>
-cudaError_t launch_scan(const TmixArgs& a, cudaStream_t s) {
-    constexpr int ROWS = NCW * 8 * RPL;
-    constexpr size_t smem = sizeof(Smem<ROWS, REV>);
-    const cudaError_t e = allow_smem<tmix_scan_kernel<T, RPL, NCW, REV>>(smem);
-    if (e != cudaSuccess) return e;
-    tmix_scan_kernel<T, RPL, NCW, REV><<<a.S * a.H * (kHead / ROWS), (NCW + NPW) * 32, smem, s>>>(a);
-    return cudaGetLastError();
-}
-
 template <typename T, bool REV>
-cudaError_t scan_by_size(const TmixArgs& a, cudaStream_t s) {
-#ifndef VAR_RPL
-#define VAR_RPL 2
-#define VAR_NCW 4
-#endif
-    return launch_scan<T, VAR_RPL, VAR_NCW, REV>(a, s);
+cudaError_t launch_scan(const TmixArgs& a, cudaStream_t s) {
+    constexpr int smem = sizeof(Smem<T, REV>);
+    static_assert(smem <= 227 * 1024);
+    const cudaError_t e = allow_smem<tmix_scan_kernel<T, REV>>(smem);
+    if (e != cudaSuccess) return e;
+    tmix_scan_kernel<T, REV><<<a.S * a.H, 128 * (1 + GROUPS), smem, s>>>(a);
+    return cudaGetLastError();
 }
 
 // ------------------------------------------------------------ single token --
@@ -374,8 +728,8 @@ __global__ void __launch_bounds__(128) tmix_step_kernel(const TmixArgs p) {
 }  // namespace
 
 cudaError_t launch_tmix_scan(const TmixArgs& a, bool half, bool reverse, cudaStream_t s) {
-    if (half) return reverse ? scan_by_size<__half, true>(a, s) : scan_by_size<__half, false>(a, s);
-    return reverse ? scan_by_size<float, true>(a, s) : scan_by_size<float, false>(a, s);
+    if (half) return reverse ? launch_scan<__half, true>(a, s) : launch_scan<__half, false>(a, s);
+    return reverse ? launch_scan<float, true>(a, s) : launch_scan<float, false>(a, s);
 }
 
 cudaError_t launch_tmix_step(const TmixArgs& a, bool half, cudaStream_t s) {

@@ -107,13 +107,19 @@ __device__ __forceinline__ float decay_gate(float d) {
 // w - 1: the update w S = S + (w - 1) S then rounds S once, and a decay near 1
 // keeps its distance from 1 over thousands of steps (w itself, rounded to 24
 // bits, would be off by up to 2^-25 in every step, in the same direction).
-// e^x - 1 by its series x (1 + x/2 (1 + x/3 (...))): -0.61 <= x <= 0, so ten
-// terms leave less than 0.61^10 / 11! < 2^-32 of it.
+// e^x - 1 by its series x (1 + x/2! + x^2/3! + ...): -0.61 <= x <= 0, so nine
+// terms leave less than 0.61^9 / 10! < 2^-27 of it.
 __device__ __forceinline__ float decay_m1(float d) {
     const float x = -kDecay * decay_gate(d);
-    float p = fmaf(x, 1.f / 10.f, 1.f);
-#pragma unroll
-    for (int n = 9; n >= 2; --n) p = fmaf(x * p, 1.f / n, 1.f);
+    float p = 1.f / 362880.f;
+    p = fmaf(p, x, 1.f / 40320.f);
+    p = fmaf(p, x, 1.f / 5040.f);
+    p = fmaf(p, x, 1.f / 720.f);
+    p = fmaf(p, x, 1.f / 120.f);
+    p = fmaf(p, x, 1.f / 24.f);
+    p = fmaf(p, x, 1.f / 6.f);
+    p = fmaf(p, x, 0.5f);
+    p = fmaf(p, x, 1.f);
     return x * p;
 }
 

@@ -27,6 +27,10 @@ namespace {
 constexpr int C = kTmixChunk;
 constexpr int LD = kHead + 4;                // row stride: 8 rows' 16-byte pieces meet no bank twice
 constexpr int LM = C + 4;
+#ifndef VAR_U
+#define VAR_U 1
+#endif
+constexpr int U = VAR_U;
 constexpr int THREADS = 256;
 
 struct Smem {
@@ -56,7 +60,7 @@ struct Lane {
 
 // X [16, 64] times Y [64, 64]^T, tall
 __device__ __forceinline__ void mul_nt(Tile& a, const Lane& l, const float (*X)[LD], const float (*Y)[LD]) {
-#pragma unroll 4
+#pragma unroll U
     for (int k = 0; k < kHead; k += 4) {
         float4 x[4], y[4];
 #pragma unroll
@@ -82,7 +86,7 @@ __device__ __forceinline__ void rank1(Tile& a, const float f[4], float4 y) {
 // X [16, N] times Y [N, 64], wide; X has row stride LX
 template <int N, int LX>
 __device__ __forceinline__ void mul_nn(Tile& a, const Lane& l, const float (*X)[LX], const float (*Y)[LD]) {
-#pragma unroll 4
+#pragma unroll U
     for (int k = 0; k < N; k += 4) {
         float4 x[4];
 #pragma unroll
@@ -96,7 +100,7 @@ __device__ __forceinline__ void mul_nn(Tile& a, const Lane& l, const float (*X)[
 }
 // M [16, 16]^T times Y [16, 64], wide
 __device__ __forceinline__ void mul_tn(Tile& a, const Lane& l, const float (*M)[LM], const float (*Y)[LD]) {
-#pragma unroll 4
+#pragma unroll U
     for (int k = 0; k < C; ++k) {
         const float4 x = ld4(&M[k][4 * l.tg]);
         const float f[4] = {x.x, x.y, x.z, x.w};
@@ -105,7 +109,7 @@ __device__ __forceinline__ void mul_tn(Tile& a, const Lane& l, const float (*M)[
 }
 // the same, tall
 __device__ __forceinline__ void mul_tn_tall(Tile& a, const Lane& l, const float (*M)[LM], const float (*Y)[LD]) {
-#pragma unroll 4
+#pragma unroll U
     for (int k = 0; k < C; ++k) {
         const float4 x = ld4(&M[k][4 * l.tg]);
         const float f[4] = {x.x, x.y, x.z, x.w};
@@ -113,7 +117,7 @@ __device__ __forceinline__ void mul_tn_tall(Tile& a, const Lane& l, const float 
     }
 }
 __device__ __forceinline__ void mul_nn_tall(Tile& a, const Lane& l, const float (*M)[LM], const float (*Y)[LD]) {
-#pragma unroll 4
+#pragma unroll U
     for (int k = 0; k < C; ++k) {
         const float f[4] = {M[l.row(0)][k], M[l.row(1)][k], M[l.row(2)][k], M[l.row(3)][k]};
         rank1(a, f, make_float4(Y[k][l.tall(0)], Y[k][l.tall(1)], Y[k][l.tall(2)], Y[k][l.tall(3)]));
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
     const int mt = tid >> 4, ms = tid & 15;
     {
         float ab = 0.f, ak = 0.f, rb = 0.f, rk = 0.f, yv = 0.f;
-#pragma unroll 4
+#pragma unroll U
         for (int k = 0; k < kHead; k += 4) {
             const float4 A = ld4(&sm.A[mt][k]), R = ld4(&sm.R[mt][k]), Y = ld4(&sm.dY[mt][k]);
             const float4 B = ld4(&sm.B[ms][k]), K = ld4(&sm.K[ms][k]), V = ld4(&sm.V[ms][k]);
@@ -263,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
     __syncthreads();
     {
         float yu = 0.f, eu = 0.f, ev = 0.f;
-#pragma unroll 4
+#pragma unroll U
         for (int k = 0; k < kHead; k += 4) {
             const float4 Y = ld4(&sm.dY[mt][k]), E = ld4(&sm.E[mt][k]);
             const float4 U = ld4(&sm.U[ms][k]), V = ld4(&sm.V[ms][k]);
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
         mul_nn<C, LM>(acc, l, sm.yv, sm.K);
         float z = 0.f;
         const int j = tid - 6 * 32;                      // 64 threads, one channel each
-#pragma unroll 8
+#pragma unroll 4
         for (int i = 0; i < kHead; ++i) z = fmaf(sm.S0[i][j], sm.G[i][j], z);
         sm.z[j] = z;
     }
