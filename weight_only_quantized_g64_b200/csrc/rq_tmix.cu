@@ -12,9 +12,10 @@
 // matrix products only, and the rows of S still do not meet.  Four warps hold 16
 // rows of S each, in the registers of the tensor cores' accumulators, which are
 // also their first operand once the summed index is taken in the order 2q, 2q+1
-// instead of q, q+4.  Three groups of four warps prepare A', R', B, K', M' of the
+// instead of q, q+4.  Two groups of four warps prepare A', R', B, K', M' of the
 // chunks ahead in turn (with the same products): one chunk's preparation is a
-// chain of small dependent steps, three times as long as its use.
+// chain of small dependent steps, longer than its use (one group: 1.09 ms where
+// two take 0.79 and three 0.90, which leave less to the row warps).
 //
 // fp32 on the tensor cores: every operand is split into two tf32 parts (22 bits
 // of it), and lo*hi + hi*lo + hi*hi go into the fp32 accumulator; what is lost
@@ -43,7 +44,7 @@ constexpr int C = kTmixChunk;
 constexpr int LA = kHead + 8;                // rows read 8 bytes at a time along the keys: 8 banks apart
 constexpr int LB = kHead + 4;                // rows read in pairs of tokens: 2 rows 8 banks apart
 constexpr int LS = C + 8;
-constexpr int GROUPS = 3, BUFFERS = 2;       // preparing groups, and chunks that each may have ready
+constexpr int GROUPS = 2, BUFFERS = 2;       // preparing groups, and chunks that each may have ready
 static_assert(C == 16 && kHead == 64);
 // 16-byte accesses: every row, and so every array, is a multiple of 16 bytes
 static_assert(LA % 4 == 0 && LB % 4 == 0 && LS % 4 == 0 && kHead % 8 == 0);

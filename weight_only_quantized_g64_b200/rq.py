@@ -371,6 +371,13 @@ def _tensor(call: str, name: str, t, dtype, shape, at: int):
         raise RQError(ERR_SHAPE, f"{call}: {name} is on {t.device}, not with the first tensor")
 
 
+def _like(t, dtype=None):
+    """An empty contiguous tensor of t's shape and device (of t's type if none is given)."""
+    if t.is_contiguous():
+        return torch.empty_like(t) if dtype is None or t.dtype is dtype else torch.empty_like(t, dtype=dtype)
+    return torch.empty(t.shape, dtype=dtype or t.dtype, device=t.device)
+
+
 def _on_gpu(call: str, at: int):
     if at < 0:
         raise RQError(ERR_SHAPE, f"{call}: the tensors must be on a CUDA device, not on the host")
@@ -461,7 +468,7 @@ def norm_residual(y, post: str = "none", post_group: int = 0, post_weight=None, 
     if h_out is None and h is not None:
         h_out = torch.empty_like(h)
     if x is None:
-        x = torch.empty(shape, dtype=torch.float16, device=y.device)
+        x = _like(y, torch.float16)
     st = lib().rq_norm_residual(y.data_ptr(), ld_y, M, D, _REAL[dtype], NORMS[post], post_group, _p(post_weight),
                                 _p(post_bias), eps_post, _p(add), ld_add, _p(gate), ld_gate, GATES[gate_act], _p(h),
                                 _p(alpha), NORMS[pre], _p(pre_weight), _p(pre_bias), eps_pre, _p(h_out), x.data_ptr(),
@@ -534,9 +541,10 @@ def tmix_scan(r, d, k, v, a, b, seq_start, state=None, state_out=None, slots=Non
         _tensor(c, "y", y, r.dtype, (T, H, HEAD), at)
     _on_gpu(c, at)
     if y is None:
-        y = torch.empty((T, H, HEAD), dtype=r.dtype, device=r.device)
+        y = _like(r)
     if state_out is None and slots is None:
-        state_out = torch.empty((S, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
+        state_out = torch.empty_like(state) if state is not None else \
+            torch.empty((S, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
     _check(lib().rq_tmix_scan(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), T, H, ld, _REAL[r.dtype], _p(seq_start), S,
                               _p(state), _p(state_out), _p(slots), n, _p(y), _p(ckpt), _p(dev_status),
                               _stream_of(at)), c)
@@ -560,9 +568,10 @@ def tmix_scan_bwd(r, d, k, v, a, b, seq_start, ckpt, dy, dstate_out=None, grads=
         _tensor(c, f"grads[{i}]", g, r.dtype, (T, H, HEAD), at)
     _on_gpu(c, at)
     if grads is None:
-        grads = tuple(torch.empty((T, H, HEAD), dtype=r.dtype, device=r.device) for _ in range(6))
+        grads = tuple(torch.empty_like(dy) for _ in range(6))
     if dstate is None:
-        dstate = torch.empty((S, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
+        dstate = torch.empty_like(dstate_out) if dstate_out is not None else \
+            torch.empty((S, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
     work = torch.empty_like(ckpt)
     _check(lib().rq_tmix_scan_bwd(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), T, H, ld, _REAL[r.dtype],
                                   _p(seq_start), S, _p(ckpt), _p(dy), _p(dstate_out), _p(dstate),
@@ -581,9 +590,10 @@ def tmix_step(r, d, k, v, a, b, state=None, state_out=None, slots=None, y=None, 
         _tensor(c, "y", y, r.dtype, (B, H, HEAD), at)
     _on_gpu(c, at)
     if y is None:
-        y = torch.empty((B, H, HEAD), dtype=r.dtype, device=r.device)
+        y = _like(r)
     if state_out is None and slots is None:
-        state_out = torch.empty((B, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
+        state_out = torch.empty_like(state) if state is not None else \
+            torch.empty((B, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
     _check(lib().rq_tmix_step(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), B, H, ld, _REAL[r.dtype], _p(state),
                               _p(state_out), _p(slots), n, _p(y), _p(dev_status), _stream_of(at)), c)
     return y, state_out
