@@ -18,110 +18,107 @@
 // and the decay's gradient is a sum over the later tokens of the chunk,
 //   dlogw_s = sum_{t >= s} (R dR - K dK - B dB)_t + sum_{t > s} (A dA)_t + Z,
 //   Z = sum_i (S0 + U^T B + V^T K) G            (the state behind the chunk).
-// About 50 000 fp32 FMA per token and head, all from shared memory.
+// About 800 000 multiplications per chunk and head, on the tensor cores
+// (rq_tf32.cuh): 2300 MMAs of 8 cycles over the four of an SM bound it.  With
+// plain FMAs the kernel was bound by shared-memory reads at 4 x 4 results per
+// thread: VAR_OLD us where this takes VAR_NEW (2048 tokens, 32 heads, fp16).
+// A value that is not finite may spoil the gradients of its chunk of 16 tokens.
+#include "rq_tf32.cuh"
 #include "rq_tmix.cuh"
 
 namespace rq {
 namespace {
 
 constexpr int C = kTmixChunk;
-constexpr int LD = kHead + 4;                // row stride: 8 rows' 16-byte pieces meet no bank twice
-constexpr int LM = C + 4;
-#ifndef VAR_U
-#define VAR_U 1
-#endif
-constexpr int U = VAR_U;
+constexpr int LD = kHead + 8;                // rows 8 banks apart: the pairs that eight lanes of a column group read
+constexpr int LM = C + 8;
 constexpr int THREADS = 256;
+static_assert(LD % 4 == 0 && LM % 4 == 0);   // 16-byte accesses: every row is a multiple of 16 bytes
 
-struct Smem {
+struct alignas(16) Smem {
     float R[C][LD], A[C][LD], B[C][LD], K[C][LD], V[C][LD], dY[C][LD], U[C][LD], E[C][LD], W[C][LD];
     float S0[kHead][LD], G[kHead][LD];
     float ab[C][LM], ak[C][LM], rb[C][LM], rk[C][LM], yu[C][LM], yv[C][LM], eu[C][LM], ev[C][LM];
-    float z[kHead];
+    float z[3][kHead];                       // the parts of Z: S0, U^T B, V^T K
 };
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
-    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
-}
 
-// A thread's 4 x 4 tile of a [16, 64] result: rows 4 tg + 0..3; columns
-// 4 cg + 0..3 (tile "wide") or, where both operands lie along the sum,
-// cg + 8 n (tile "tall": rows of the second operand, without bank conflicts).
-struct Tile {
-    float v[4][4];
-};
+// Half of a [16, 64] result per warp: four products of 8 columns, c[n] the
+// columns 32 half + 8 n.
+using Half = float[4][4];
 struct Lane {
-    int tg, cg, half;
-    __device__ __forceinline__ int row(int m) const { return 4 * tg + m; }
-    __device__ __forceinline__ int wide() const { return 32 * half + 4 * cg; }
-    __device__ __forceinline__ int tall(int n) const { return 32 * half + cg + 8 * n; }
+    int g, q, first;                         // first: 32 half
 };
-
-// X [16, 64] times Y [64, 64]^T, tall
-__device__ __forceinline__ void mul_nt(Tile& a, const Lane& l, const float (*X)[LD], const float (*Y)[LD]) {
-#pragma unroll U
-    for (int k = 0; k < kHead; k += 4) {
-        float4 x[4], y[4];
+__device__ __forceinline__ void clear(Half& c) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) x[m] = ld4(&X[l.row(m)][k]);
+    for (int n = 0; n < 4; ++n) zero(c[n]);
+}
+// c += X Y^T, X [16, 64], Y [64, 64]
+__device__ __forceinline__ void times_rows(Half& c, const Lane& l, const float (*X)[LD], const float (*Y)[LD]) {
+#pragma unroll 2
+    for (int k = 0; k < kHead; k += 8) {
+        float4 b[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) y[n] = ld4(&Y[l.tall(n)][k]);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) a.v[m][n] = dot4(x[m], y[n], a.v[m][n]);
+        for (int n = 0; n < 4; ++n) b[n] = along(&Y[l.first + 8 * n + l.g][k + 2 * l.q]);
+        products<4>(c, rows_at(X, l.g, k + 2 * l.q), b);
     }
 }
-// one row of the second operand times four factors, wide
-__device__ __forceinline__ void rank1(Tile& a, const float f[4], float4 y) {
+// c += X Y, X [16, N] (or, TRANSPOSED, of X [N, 16] the columns), Y [N, 64]
+template <int N, bool TRANSPOSED, int LX>
+__device__ __forceinline__ void times(Half& c, const Lane& l, const float (*X)[LX], const float (*Y)[LD]) {
+#pragma unroll 2
+    for (int k = 0; k < N; k += 8) {
+        float4 b[4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        a.v[m][0] = fmaf(f[m], y.x, a.v[m][0]);
-        a.v[m][1] = fmaf(f[m], y.y, a.v[m][1]);
-        a.v[m][2] = fmaf(f[m], y.z, a.v[m][2]);
-        a.v[m][3] = fmaf(f[m], y.w, a.v[m][3]);
+        for (int n = 0; n < 4; ++n) b[n] = down(&Y[k + 2 * l.q][l.first + 8 * n + l.g], LD);
+        products<4>(c, TRANSPOSED ? columns_at(X, l.g, k + 2 * l.q) : rows_at(X, l.g, k + 2 * l.q), b);
     }
 }
-// X [16, N] times Y [N, 64], wide; X has row stride LX
-template <int N, int LX>
-__device__ __forceinline__ void mul_nn(Tile& a, const Lane& l, const float (*X)[LX], const float (*Y)[LD]) {
-#pragma unroll U
-    for (int k = 0; k < N; k += 4) {
-        float4 x[4];
+// m = X Y^T, both [16, 64], what lies above the diagonal (or on it, STRICT) zero
+__device__ __forceinline__ void square(float (*m)[LM], const Lane& l, const float (*X)[LD], const float (*Y)[LD],
+                                       bool strict) {
+    float c[4][4];                           // two column halves, each as two sums
 #pragma unroll
-        for (int m = 0; m < 4; ++m) x[m] = ld4(&X[l.row(m)][k]);
+    for (int n = 0; n < 4; ++n) zero(c[n]);
+#pragma unroll 2
+    for (int k = 0; k < kHead; k += 16) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const float f[4] = {(&x[0].x)[kk], (&x[1].x)[kk], (&x[2].x)[kk], (&x[3].x)[kk]};
-            rank1(a, f, ld4(&Y[k + kk][l.wide()]));
+        for (int i = 0; i < 2; ++i) {
+            const int at = k + 8 * i + 2 * l.q;
+            const float4 b[2] = {along(&Y[l.g][at]), along(&Y[8 + l.g][at])};
+            products<2>(c + 2 * i, rows_at(X, l.g, at), b);
         }
     }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = l.g + 8 * (j >> 1), s = 8 * n + 2 * l.q + (j & 1);
+            m[t][s] = t > s || (t == s && !strict) ? c[n][j] + c[n + 2][j] : 0.f;
+        }
 }
-// M [16, 16]^T times Y [16, 64], wide
-__device__ __forceinline__ void mul_tn(Tile& a, const Lane& l, const float (*M)[LM], const float (*Y)[LD]) {
-#pragma unroll U
-    for (int k = 0; k < C; ++k) {
-        const float4 x = ld4(&M[k][4 * l.tg]);
-        const float f[4] = {x.x, x.y, x.z, x.w};
-        rank1(a, f, ld4(&Y[k][l.wide()]));
+__device__ __forceinline__ void put(const Half& c, const Lane& l, float (*to)[LD]) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const int k = l.first + 8 * n + 2 * l.q;
+        *reinterpret_cast<float2*>(&to[l.g][k]) = make_float2(c[n][0], c[n][1]);
+        *reinterpret_cast<float2*>(&to[l.g + 8][k]) = make_float2(c[n][2], c[n][3]);
     }
 }
-// the same, tall
-__device__ __forceinline__ void mul_tn_tall(Tile& a, const Lane& l, const float (*M)[LM], const float (*Y)[LD]) {
-#pragma unroll U
-    for (int k = 0; k < C; ++k) {
-        const float4 x = ld4(&M[k][4 * l.tg]);
-        const float f[4] = {x.x, x.y, x.z, x.w};
-        rank1(a, f, make_float4(Y[k][l.tall(0)], Y[k][l.tall(1)], Y[k][l.tall(2)], Y[k][l.tall(3)]));
-    }
-}
-__device__ __forceinline__ void mul_nn_tall(Tile& a, const Lane& l, const float (*M)[LM], const float (*Y)[LD]) {
-#pragma unroll U
-    for (int k = 0; k < C; ++k) {
-        const float f[4] = {M[l.row(0)][k], M[l.row(1)][k], M[l.row(2)][k], M[l.row(3)][k]};
-        rank1(a, f, make_float4(Y[k][l.tall(0)], Y[k][l.tall(1)], Y[k][l.tall(2)], Y[k][l.tall(3)]));
-    }
+// sum over the 16 tokens of c times X, into z
+__device__ __forceinline__ void weigh(const Half& c, const Lane& l, const float (*X)[LD], float* z) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int k = l.first + 8 * n + 2 * l.q + j;
+            float s = fmaf(c[n][j], X[l.g][k], c[n][j + 2] * X[l.g + 8][k]);
+            s += __shfl_xor_sync(0xffffffffu, s, 4);
+            s += __shfl_xor_sync(0xffffffffu, s, 8);
+            s += __shfl_xor_sync(0xffffffffu, s, 16);
+            if (l.g == 0) z[k] = s;
+        }
 }
 
 template <typename T>
@@ -156,33 +153,35 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
     const int64_t in_at = (t0 + et) * p.ld + static_cast<int64_t>(h) * kHead + ec;
     const int64_t out_at = ((t0 + et) * p.H + h) * kHead + ec;
     const bool in = et < nt;
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto get = [&](int i) { return in ? load4(static_cast<const T*>(p.in[i]) + in_at) : zero; };
-    const float4 xr = get(0), xd = get(1), xk = get(2), xv = get(3), xa = get(4), xb = get(5);
-    const float4 xy = in ? load4(static_cast<const T*>(p.dy) + out_at) : zero;
-    *reinterpret_cast<float4*>(&sm.V[et][ec]) = xv;
-    *reinterpret_cast<float4*>(&sm.dY[et][ec]) = xy;
-    *reinterpret_cast<float4*>(&sm.W[et][ec]) =
-        in ? make_float4(decay_m1(xd.x), decay_m1(xd.y), decay_m1(xd.z), decay_m1(xd.w)) : zero;
-    __syncthreads();
-    if (tid < kHead) {                                   // W_t
-        float w = 1.f;
-#pragma unroll
-        for (int t = 0; t < C; ++t) {
-            w = fmaf(w, sm.W[t][tid], w);
-            sm.W[t][tid] = w;
-        }
-    }
-    __syncthreads();
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto get = [&](int i) { return in ? load4(static_cast<const T*>(p.in[i]) + in_at) : none; };
     const auto mul = [](float4 x, float4 y) { return make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w); };
+    const auto row4 = [&](float (*to)[LD], float4 v) { *reinterpret_cast<float4*>(&to[et][ec]) = v; };
+    float4 xd;
     {
+        const float4 xr = get(0), xk = get(2), xv = get(3), xa = get(4), xb = get(5);
+        xd = get(1);
+        const float4 xy = in ? load4(static_cast<const T*>(p.dy) + out_at) : none;
+        row4(sm.V, xv);
+        row4(sm.dY, xy);
+        row4(sm.W, in ? make_float4(decay_m1(xd.x), decay_m1(xd.y), decay_m1(xd.z), decay_m1(xd.w)) : none);
+        __syncthreads();
+        if (tid < kHead) {                               // W_t
+            float w = 1.f;
+#pragma unroll
+            for (int t = 0; t < C; ++t) {
+                w = fmaf(w, sm.W[t][tid], w);
+                sm.W[t][tid] = w;
+            }
+        }
+        __syncthreads();
         const float4 w = ld4(&sm.W[et][ec]);
         const float4 wp = et ? ld4(&sm.W[et - 1][ec]) : make_float4(1.f, 1.f, 1.f, 1.f);
         const float4 iw = make_float4(1.f / w.x, 1.f / w.y, 1.f / w.z, 1.f / w.w);
-        *reinterpret_cast<float4*>(&sm.R[et][ec]) = mul(xr, w);
-        *reinterpret_cast<float4*>(&sm.A[et][ec]) = mul(xa, wp);
-        *reinterpret_cast<float4*>(&sm.B[et][ec]) = mul(xb, iw);
-        *reinterpret_cast<float4*>(&sm.K[et][ec]) = mul(xk, iw);
+        row4(sm.R, mul(xr, w));
+        row4(sm.A, mul(xa, wp));
+        row4(sm.B, mul(xb, iw));
+        row4(sm.K, mul(xk, iw));
         for (int i = tid; i < kHead * kHead / 4; i += THREADS) {
             const int r = i >> 4, c = (i & 15) * 4;
             float4* g = reinterpret_cast<float4*>(&sm.G[r][c]);
@@ -191,54 +190,43 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
     }
     __syncthreads();
 
-    // ---- the 16 x 16 products that need no solution
-    const int mt = tid >> 4, ms = tid & 15;
-    {
-        float ab = 0.f, ak = 0.f, rb = 0.f, rk = 0.f, yv = 0.f;
-#pragma unroll U
-        for (int k = 0; k < kHead; k += 4) {
-            const float4 A = ld4(&sm.A[mt][k]), R = ld4(&sm.R[mt][k]), Y = ld4(&sm.dY[mt][k]);
-            const float4 B = ld4(&sm.B[ms][k]), K = ld4(&sm.K[ms][k]), V = ld4(&sm.V[ms][k]);
-            ab = dot4(A, B, ab);
-            ak = dot4(A, K, ak);
-            rb = dot4(R, B, rb);
-            rk = dot4(R, K, rk);
-            yv = dot4(Y, V, yv);
+    // ---- the 16 x 16 products that need no solution; two warps begin dR, one takes S0's part of Z
+    const int warp = tid >> 5, lane = tid & 31, pair = warp >> 1;
+    const Lane l = {lane >> 2, lane & 3, 32 * (warp & 1)};
+    Half acc;
+    clear(acc);
+    if (warp == 0) square(sm.ab, l, sm.A, sm.B, true);
+    else if (warp == 1) square(sm.ak, l, sm.A, sm.K, true);
+    else if (warp == 2) square(sm.rb, l, sm.R, sm.B, false);
+    else if (warp == 3) square(sm.rk, l, sm.R, sm.K, false);
+    else if (warp == 4) square(sm.yv, l, sm.dY, sm.V, false);
+    else if (warp >= 6) times<kHead, false>(acc, l, sm.dY, sm.S0);
+    else {
+        float z0 = 0.f, z1 = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < kHead; ++i) {
+            z0 = fmaf(sm.S0[i][lane], sm.G[i][lane], z0);
+            z1 = fmaf(sm.S0[i][32 + lane], sm.G[i][32 + lane], z1);
         }
-        sm.ab[mt][ms] = mt > ms ? ab : 0.f;
-        sm.ak[mt][ms] = mt > ms ? ak : 0.f;
-        sm.rb[mt][ms] = mt >= ms ? rb : 0.f;
-        sm.rk[mt][ms] = mt >= ms ? rk : 0.f;
-        sm.yv[mt][ms] = mt >= ms ? yv : 0.f;
+        sm.z[0][lane] = z0;
+        sm.z[0][32 + lane] = z1;
     }
     __syncthreads();
 
     // ---- right-hand sides; each pair of warps takes one [16, 64] result
-    const int warp = tid >> 5, lane = tid & 31, pair = warp >> 1;
-    const Lane l = {lane >> 3, lane & 7, warp & 1};
-    Tile acc;
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) acc.v[m][n] = 0.f;
     if (pair == 0) {
-        mul_nt(acc, l, sm.A, sm.S0);
-        mul_nn_tall(acc, l, sm.ak, sm.V);
+        times_rows(acc, l, sm.A, sm.S0);
+        times<C, false>(acc, l, sm.ak, sm.V);
+        put(acc, l, sm.U);
     } else if (pair == 1) {
-        mul_nt(acc, l, sm.B, sm.G);
-        mul_tn_tall(acc, l, sm.rb, sm.dY);
+        times_rows(acc, l, sm.B, sm.G);
+        times<C, true>(acc, l, sm.rb, sm.dY);
+        put(acc, l, sm.E);
     } else if (pair == 2) {
-        mul_nt(acc, l, sm.K, sm.G);
-        mul_tn_tall(acc, l, sm.rk, sm.dY);
+        times_rows(acc, l, sm.K, sm.G);
+        times<C, true>(acc, l, sm.rk, sm.dY);
     } else {
-        mul_nn<kHead, LD>(acc, l, sm.dY, sm.S0);
-    }
-    if (pair < 2) {
-        float (*dst)[LD] = pair ? sm.E : sm.U;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) dst[l.row(m)][l.tall(n)] = acc.v[m][n];
+        times<C, false>(acc, l, sm.yv, sm.K);            // dR: all but its part with U
     }
     __syncthreads();
 
@@ -265,124 +253,87 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
         for (int t = 0; t < C - 1; ++t) sm.E[t][tid - kHead] = e[t];
     }
     __syncthreads();
-    {
-        float yu = 0.f, eu = 0.f, ev = 0.f;
-#pragma unroll U
-        for (int k = 0; k < kHead; k += 4) {
-            const float4 Y = ld4(&sm.dY[mt][k]), E = ld4(&sm.E[mt][k]);
-            const float4 U = ld4(&sm.U[ms][k]), V = ld4(&sm.V[ms][k]);
-            yu = dot4(Y, U, yu);
-            eu = dot4(E, U, eu);
-            ev = dot4(E, V, ev);
-        }
-        sm.yu[mt][ms] = mt >= ms ? yu : 0.f;
-        sm.eu[mt][ms] = mt > ms ? eu : 0.f;
-        sm.ev[mt][ms] = mt > ms ? ev : 0.f;
+
+    // ---- the parts that need no more 16 x 16 products, and those products
+    if (pair < 2) clear(acc);
+    if (pair == 0) times<kHead, false>(acc, l, sm.E, sm.S0);             // dA
+    else if (pair == 1) {                                                // dB
+        times<kHead, false>(acc, l, sm.U, sm.G);
+        weigh(acc, l, sm.B, sm.z[1]);
+    } else if (warp == 4) square(sm.yu, l, sm.dY, sm.U, false);
+    else if (warp == 5) square(sm.eu, l, sm.E, sm.U, true);
+    else if (warp == 6) square(sm.ev, l, sm.E, sm.V, true);
+    if (pair == 2) times<C, true>(acc, l, sm.ak, sm.E);                  // dV
+    __syncthreads();
+    Half more;                                                           // dK, of the pair that has dV
+    if (pair == 0) {
+        times<C, false>(acc, l, sm.eu, sm.B);
+        times<C, false>(acc, l, sm.ev, sm.K);
+    } else if (pair == 1) {
+        times<C, true>(acc, l, sm.yu, sm.R);
+        times<C, true>(acc, l, sm.eu, sm.A);
+    } else if (pair == 2) {
+        clear(more);
+        times<kHead, false>(more, l, sm.V, sm.G);
+        weigh(more, l, sm.K, sm.z[2]);
+        times<C, true>(more, l, sm.yv, sm.R);
+        times<C, true>(more, l, sm.ev, sm.A);
+    } else {
+        times<C, false>(acc, l, sm.yu, sm.B);
     }
+    __syncthreads();                                     // S0 and G are free from here
+    float (*dA)[LD] = &sm.S0[0], (*dB)[LD] = &sm.S0[16], (*dV)[LD] = &sm.S0[32], (*dR)[LD] = &sm.S0[48];
+    float (*dK)[LD] = &sm.G[0], (*dl)[LD] = &sm.G[16];
+    put(acc, l, pair == 0 ? dA : pair == 1 ? dB : pair == 2 ? dV : dR);
+    if (pair == 2) put(more, l, dK);
     __syncthreads();
 
-    // ---- gradients.  decay[]: what each product adds to the decay's gradient, per token and channel
-    T* const out[6] = {static_cast<T*>(p.out[0]), static_cast<T*>(p.out[1]), static_cast<T*>(p.out[2]),
-                       static_cast<T*>(p.out[3]), static_cast<T*>(p.out[4]), static_cast<T*>(p.out[5])};
-    const auto at = [&](int t) { return ((t0 + t) * p.H + h) * kHead; };
-    if (pair == 2) {                                     // dV: add M(A K^T)^T E to the held sum
-        mul_tn_tall(acc, l, sm.ak, sm.E);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-                if (l.row(m) < nt) out[3][at(l.row(m)) + l.tall(n)] = from_f32<T>(acc.v[m][n]);
-    }
-    if (pair < 3) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) acc.v[m][n] = 0.f;
-    }
-    float zpart[4] = {0.f, 0.f, 0.f, 0.f};               // sum over this thread's rows of (B or K) times (U G or V G)
-    if (pair == 0) {                                     // dA
-        mul_nn<kHead, LD>(acc, l, sm.E, sm.S0);
-        mul_nn<C, LM>(acc, l, sm.eu, sm.B);
-        mul_nn<C, LM>(acc, l, sm.ev, sm.K);
-    } else if (pair == 1) {                              // dB
-        mul_nn<kHead, LD>(acc, l, sm.U, sm.G);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) zpart[n] = fmaf(acc.v[m][n], sm.B[l.row(m)][l.wide() + n], zpart[n]);
-        mul_tn(acc, l, sm.yu, sm.R);
-        mul_tn(acc, l, sm.eu, sm.A);
-    } else if (pair == 2) {                              // dK
-        mul_nn<kHead, LD>(acc, l, sm.V, sm.G);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) zpart[n] = fmaf(acc.v[m][n], sm.K[l.row(m)][l.wide() + n], zpart[n]);
-        mul_tn(acc, l, sm.yv, sm.R);
-        mul_tn(acc, l, sm.ev, sm.A);
-    } else {                                             // dR
-        mul_nn<C, LM>(acc, l, sm.yu, sm.B);
-        mul_nn<C, LM>(acc, l, sm.yv, sm.K);
-        float z = 0.f;
-        const int j = tid - 6 * 32;                      // 64 threads, one channel each
-#pragma unroll 4
-        for (int i = 0; i < kHead; ++i) z = fmaf(sm.S0[i][j], sm.G[i][j], z);
-        sm.z[j] = z;
-    }
-    // the four row groups of a warp add their parts of Z in a fixed order
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        zpart[n] += __shfl_xor_sync(0xffffffffu, zpart[n], 8);
-        zpart[n] += __shfl_xor_sync(0xffffffffu, zpart[n], 16);
-    }
-    float4 own[4];                                       // this product's operand rows, before they are overwritten
+    // ---- out, and what each token adds to the decay's gradient
     {
-        const float (*X)[LD] = pair == 0 ? sm.A : pair == 1 ? sm.B : pair == 2 ? sm.K : sm.R;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) own[m] = ld4(&X[l.row(m)][l.wide()]);
-    }
-    __syncthreads();                                     // U, E, S0 and G are free from here
-    float (*dl)[LD] = &sm.S0[16 * pair];                 // four [16, 64] arrays in the place of S0
-    {
-        T* o = out[pair == 0 ? 4 : pair == 1 ? 5 : pair == 2 ? 2 : 0];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int t = l.row(m);
-            const float4 g = make_float4(acc.v[m][0], acc.v[m][1], acc.v[m][2], acc.v[m][3]);
-            *reinterpret_cast<float4*>(&dl[t][l.wide()]) = mul(own[m], g);
-            float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (pair != 0) w = ld4(&sm.W[t][l.wide()]);
-            else if (t > 0) w = ld4(&sm.W[t - 1][l.wide()]);
-            if (pair == 1 || pair == 2) w = make_float4(1.f / w.x, 1.f / w.y, 1.f / w.z, 1.f / w.w);
-            if (t < nt) store4(o + at(t) + l.wide(), mul(g, w));
+        const float4 w = ld4(&sm.W[et][ec]);
+        const float4 wp = et ? ld4(&sm.W[et - 1][ec]) : make_float4(1.f, 1.f, 1.f, 1.f);
+        const float4 iw = make_float4(1.f / w.x, 1.f / w.y, 1.f / w.z, 1.f / w.w);
+        const float4 gr = ld4(&dR[et][ec]), gk = ld4(&dK[et][ec]), gb = ld4(&dB[et][ec]);
+        float4 d = mul(ld4(&sm.R[et][ec]), gr);
+        const float4 dk = mul(ld4(&sm.K[et][ec]), gk), db = mul(ld4(&sm.B[et][ec]), gb);
+        d = make_float4(d.x - dk.x - db.x, d.y - dk.y - db.y, d.z - dk.z - db.z, d.w - dk.w - db.w);
+        if (et + 1 < C) {
+            const float4 n = mul(ld4(&sm.A[et + 1][ec]), ld4(&dA[et + 1][ec]));
+            d = make_float4(d.x + n.x, d.y + n.y, d.z + n.z, d.w + n.w);
         }
-        if ((pair == 1 || pair == 2) && l.tg == 0)
-            *reinterpret_cast<float4*>(&sm.G[pair][l.wide()]) = make_float4(zpart[0], zpart[1], zpart[2], zpart[3]);
+        row4(dl, d);
+        if (in) {
+            const auto out = [&](int i, float4 v) { store4(static_cast<T*>(p.out[i]) + out_at, v); };
+            out(0, mul(gr, w));
+            out(2, mul(gk, iw));
+            out(3, ld4(&dV[et][ec]));
+            out(4, mul(ld4(&dA[et][ec]), wp));
+            out(5, mul(gb, iw));
+        }
     }
     __syncthreads();
     if (tid < kHead) {
-        const float (*dA)[LD] = &sm.S0[0], (*dB)[LD] = &sm.S0[16], (*dK)[LD] = &sm.S0[32], (*dR)[LD] = &sm.S0[48];
-        float sum = sm.z[tid] + sm.G[1][tid] + sm.G[2][tid];
+        float sum = sm.z[0][tid] + sm.z[1][tid] + sm.z[2][tid];
 #pragma unroll
         for (int t = C - 1; t >= 0; --t) {
-            sum += (dR[t][tid] - dK[t][tid]) - dB[t][tid];
-            if (t + 1 < C) sum += dA[t + 1][tid];
-            sm.E[t][tid] = sum;
+            sum += dl[t][tid];
+            dl[t][tid] = sum;
         }
     }
     __syncthreads();
     if (in) {
-        const float4 g = ld4(&sm.E[et][ec]);
+        const float4 g = ld4(&dl[et][ec]);
         const auto dd = [](float dlogw, float d) {
             const float s = decay_gate(d);
             return dlogw * (-kDecay * s * (1.f - s));
         };
-        store4(out[1] + out_at, make_float4(dd(g.x, xd.x), dd(g.y, xd.y), dd(g.z, xd.z), dd(g.w, xd.w)));
+        store4(static_cast<T*>(p.out[1]) + out_at, make_float4(dd(g.x, xd.x), dd(g.y, xd.y), dd(g.z, xd.z), dd(g.w, xd.w)));
     }
 }
 
 template <typename T>
 cudaError_t launch(const TmixArgs& a, cudaStream_t s) {
+    static_assert(sizeof(Smem) <= 113 * 1024, "two CTAs per SM");
     const cudaError_t e = allow_smem<tmix_chunk_bwd_kernel<T>>(sizeof(Smem));
     if (e != cudaSuccess) return e;
     const int64_t places = a.T / C + a.S;
