@@ -50,19 +50,41 @@ __device__ __forceinline__ Rows rows_of(float g0, float g1, float h0, float h1) 
     return r;
 }
 // N products of one step: the second operands are elements 2q and 2q + 1 of the
-// step, column g, as quads.  One part after the other over all N, as an MMA waits
-// 21 cycles for the one before it on the same sum.  EXACT: the first operand is
-// its hi part.
-template <int N, bool EXACT = false>
-__device__ __forceinline__ void products(float (*c)[4], const Rows& a, const float4 (&b)[N]) {
+// step, column g, as quads.  The sums of the small parts are kept apart: the
+// tensor cores cut every sum off (instead of rounding it), and the large one is
+// then cut once a step instead of three times.  One part after the other over all
+// N, as an MMA waits 21 cycles for the one before it on the same sum.  EXACT: the
+// first operand is its hi part.
+template <int N>
+struct Sums {
+    float c[N][4], small[N][4];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[n][j] = small[n][j] = 0.f;
+    }
+    __device__ __forceinline__ float at(int n, int j) const { return c[n][j] + small[n][j]; }
+    __device__ __forceinline__ void fold() {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                c[n][j] += small[n][j];
+                small[n][j] = 0.f;
+            }
+    }
+};
+template <bool EXACT = false, int N>
+__device__ __forceinline__ void products(Sums<N>& s, const Rows& a, const float4 (&b)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma(s.small[n], a.hi, __float_as_uint(b[n].z), __float_as_uint(b[n].w));
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma(s.c[n], a.hi, __float_as_uint(b[n].x), __float_as_uint(b[n].y));
     if (!EXACT) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) mma(c[n], a.lo, __float_as_uint(b[n].x), __float_as_uint(b[n].y));
+        for (int n = 0; n < N; ++n) mma(s.small[n], a.lo, __float_as_uint(b[n].x), __float_as_uint(b[n].y));
     }
-#pragma unroll
-    for (int n = 0; n < N; ++n) mma(c[n], a.hi, __float_as_uint(b[n].z), __float_as_uint(b[n].w));
-#pragma unroll
-    for (int n = 0; n < N; ++n) mma(c[n], a.hi, __float_as_uint(b[n].x), __float_as_uint(b[n].y));
 }
 // Second operands from a matrix whose rows are the columns of the product (two
 // neighbours of a row), and from one whose rows are the summed index (two rows).
@@ -80,6 +102,5 @@ template <int LD>
 __device__ __forceinline__ Rows columns_at(const float (*m)[LD], int g, int k) {  // of the transposed matrix
     return rows_of(m[k][g], m[k + 1][g], m[k][g + 8], m[k + 1][g + 8]);
 }
-__device__ __forceinline__ void zero(float (&c)[4]) { c[0] = c[1] = c[2] = c[3] = 0.f; }
 
 }  // namespace rq

@@ -215,31 +215,23 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
         const int lx = second || !REV ? LA : LB;
         const float* z = REV ? &sm.x[0][0] : warp & 1 ? &ch.k[0][0] : &ch.b[0][0];
         const int lz = REV ? LA : LB;
-        float c[4][4];                       // two column halves, each as two sums
-#pragma unroll
-        for (int n = 0; n < 4; ++n) zero(c[n]);
-#pragma unroll 2
-        for (int k = 0; k < kHead; k += 16) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float* row = x + g * lx + k + 8 * i + 2 * q;
-                const float2 u = *reinterpret_cast<const float2*>(row), v = *reinterpret_cast<const float2*>(row + 8 * lx);
-                const float* col = z + g * lz + k + 8 * i + 2 * q;
-                const float4 b[2] = {along(col), along(col + 8 * lz)};
-                products<2>(c + 2 * i, rows_of(u.x, u.y, v.x, v.y), b);
-            }
+        Sums<2> c;                           // two column halves
+        c.clear();
+#pragma unroll 4
+        for (int k = 0; k < kHead; k += 8) {
+            const float* row = x + g * lx + k + 2 * q;
+            const float2 u = *reinterpret_cast<const float2*>(row), v = *reinterpret_cast<const float2*>(row + 8 * lx);
+            const float* col = z + g * lz + k + 2 * q;
+            const float4 b[2] = {along(col), along(col + 8 * lz)};
+            products(c, rows_of(u.x, u.y, v.x, v.y), b);
         }
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[n][j] += c[n + 2][j];
         const int what = REV ? 2 * warp : warp;              // 0: A B^T, 1: A K^T, 2: R B^T, 3: R K^T
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = g + 8 * (j >> 1), s = 8 * n + 2 * q + (j & 1);
-                const float v = t > s || (t == s && what >= 2) ? c[n][j] : 0.f;
+                const float v = t > s || (t == s && what >= 2) ? c.at(n, j) : 0.f;
                 if (what == 0) sm.abt[s][t] = v;
                 if (what == 2) sm.rb[t][s] = v;
                 if constexpr (!REV) {
@@ -282,13 +274,14 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
 
     // 16 keys per warp, in two products of 8 columns
     const int kw = warp * 16;
-    float c[2][4];
+    Sums<2> c;
     const auto put = [&](float* to, int ld) {
+        c.fold();
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             float* at = to + g * ld + kw + 8 * n + 2 * q;
-            *reinterpret_cast<float2*>(at) = make_float2(c[n][0], c[n][1]);
-            *reinterpret_cast<float2*>(at + 8 * ld) = make_float2(c[n][2], c[n][3]);
+            *reinterpret_cast<float2*>(at) = make_float2(c.c[n][0], c.c[n][1]);
+            *reinterpret_cast<float2*>(at + 8 * ld) = make_float2(c.c[n][2], c.c[n][3]);
         }
     };
     const auto take = [&](const float* from, int ld) {
@@ -296,7 +289,7 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
         for (int n = 0; n < 2; ++n) {
             const float* at = from + g * ld + kw + 8 * n + 2 * q;
             const float2 x = *reinterpret_cast<const float2*>(at), y = *reinterpret_cast<const float2*>(at + 8 * ld);
-            c[n][0] = x.x; c[n][1] = x.y; c[n][2] = y.x; c[n][3] = y.y;
+            c.c[n][0] = x.x; c.c[n][1] = x.y; c.c[n][2] = y.x; c.c[n][3] = y.y;
         }
     };
     // c += m z, or with the columns of m, z the rows of 16 tokens
@@ -305,11 +298,10 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
         for (int s = 0; s < C; s += 8) {
             const float* at = z + (s + 2 * q) * ld + kw + g;
             const float4 b[2] = {down(at, ld), down(at + 8, ld)};
-            products<2>(c, columns ? columns_at(m, g, s + 2 * q) : rows_at(m, g, s + 2 * q), b);
+            products(c, columns ? columns_at(m, g, s + 2 * q) : rows_at(m, g, s + 2 * q), b);
         }
     };
-    zero(c[0]);
-    zero(c[1]);
+    c.clear();
     if constexpr (!REV) {
         multiply(sm.t, false, &sm.x[0][0], LA);                  // A' = T A
         put(&ch.a[0][0], LA);
@@ -321,23 +313,23 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
         multiply(sm.rb, false, &ch.a[0][0], LA);
         put(&ch.r[0][0], LA);
         if (warp < 2) {                                          // M' = L(R K^T) + L(R B^T) N, 8 columns each
-            float e[1][4];
+            Sums<1> e;
+            e.clear();
             const float* at = &sm.rk[g][8 * warp + 2 * q];
             const float2 x = *reinterpret_cast<const float2*>(at), y = *reinterpret_cast<const float2*>(at + 8 * LS);
-            e[0][0] = x.x; e[0][1] = x.y; e[0][2] = y.x; e[0][3] = y.y;
+            e.c[0][0] = x.x; e.c[0][1] = x.y; e.c[0][2] = y.x; e.c[0][3] = y.y;
 #pragma unroll
             for (int s = 0; s < C; s += 8) {
                 const float4 b[1] = {down(&sm.n[s + 2 * q][8 * warp + g], LS)};
-                products<1>(e, rows_at(sm.rb, g, s + 2 * q), b);
+                products(e, rows_at(sm.rb, g, s + 2 * q), b);
             }
-            *reinterpret_cast<float2*>(&ch.m[g][8 * warp + 2 * q]) = make_float2(e[0][0], e[0][1]);
-            *reinterpret_cast<float2*>(&ch.m[g + 8][8 * warp + 2 * q]) = make_float2(e[0][2], e[0][3]);
+            *reinterpret_cast<float2*>(&ch.m[g][8 * warp + 2 * q]) = make_float2(e.at(0, 0), e.at(0, 1));
+            *reinterpret_cast<float2*>(&ch.m[g + 8][8 * warp + 2 * q]) = make_float2(e.at(0, 2), e.at(0, 3));
         }
     } else {
         multiply(sm.t, false, &ch.b[0][0], LB);                  // A' = T A
         put(&sm.y[0][0], LB);
-        zero(c[0]);                                              // B' = T^T B
-        zero(c[1]);
+        c.clear();                                               // B' = T^T B
         multiply(sm.t, true, &sm.x[0][0], LA);
         put(&ch.a[0][0], LA);
         __syncwarp();
@@ -354,20 +346,29 @@ using State = float[8][4];
 template <typename T>
 __device__ __forceinline__ void forward_chunk(State& S, const Chunk<T, false>& ch, float (*y)[C + 4], int row, int lane) {
     const int g = lane >> 2, q = lane & 3;
-    float XY[4][4];
-    float (*X)[4] = XY, (*Y)[4] = XY + 2;
+    Sums<4> XY;                              // X, then Y
     int from[2] = {C, C};                    // first token of the row whose v is not finite
-#pragma unroll
-    for (int n = 0; n < 4; ++n) zero(XY[n]);
+    XY.clear();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {            // X = S A'^T, Y = S R'^T
         const float4 b[4] = {along(&ch.a[g][8 * k + 2 * q]), along(&ch.a[8 + g][8 * k + 2 * q]),
                              along(&ch.r[g][8 * k + 2 * q]), along(&ch.r[8 + g][8 * k + 2 * q])};
-        products<4>(XY, rows_of(S[k][0], S[k][1], S[k][2], S[k][3]), b);
+        products(XY, rows_of(S[k][0], S[k][1], S[k][2], S[k][3]), b);
     }
+    XY.fold();
+    Sums<2> Y;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {            // + V^T M'^T; S += X B + V^T K'
-        const Rows x = rows_of(X[s][0], X[s][1], X[s][2], X[s][3]);
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            Y.c[n][j] = XY.c[n + 2][j];
+            Y.small[n][j] = 0.f;
+        }
+    constexpr bool EXACT = sizeof(T) == 2;
+    Rows x[2], v[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {            // Y += V^T M'^T
+        x[s] = rows_of(XY.c[s][0], XY.c[s][1], XY.c[s][2], XY.c[s][3]);
         const T *v0 = &ch.v[8 * s + 2 * q][row + g], *v1 = v0 + kHead + 8;
         float vf[4] = {to_f32(v0[0]), to_f32(v1[0]), to_f32(v0[8]), to_f32(v1[8])};
 #pragma unroll
@@ -376,20 +377,29 @@ __device__ __forceinline__ void forward_chunk(State& S, const Chunk<T, false>& c
                 vf[j] = 0.f;
                 from[j >> 1] = min(from[j >> 1], 8 * s + 2 * q + (j & 1));
             }
-        const Rows v = rows_of(vf[0], vf[1], vf[2], vf[3]);
-        constexpr bool EXACT = sizeof(T) == 2;
+        v[s] = rows_of(vf[0], vf[1], vf[2], vf[3]);
         const float4 m[2] = {along(&ch.m[g][8 * s + 2 * q]), along(&ch.m[8 + g][8 * s + 2 * q])};
-        products<2, EXACT>(Y, v, m);
+        products<EXACT>(Y, v[s], m);
+    }
+    Y.fold();
 #pragma unroll
-        for (int n = 0; n < 8; n += 4) {
+    for (int n = 0; n < 8; n += 4) {         // S += X B + V^T K'
+        Sums<4> d;
+        d.clear();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
             float4 b[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) b[i] = down(&ch.b[8 * s + 2 * q][8 * (n + i) + g], LB);
-            products<4>(S + n, x, b);
+            products(d, x[s], b);
 #pragma unroll
             for (int i = 0; i < 4; ++i) b[i] = down(&ch.k[8 * s + 2 * q][8 * (n + i) + g], LB);
-            products<4, EXACT>(S + n, v, b);
+            products<EXACT>(d, v[s], b);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[n + i][j] += d.at(i, j);
     }
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
@@ -409,14 +419,14 @@ __device__ __forceinline__ void forward_chunk(State& S, const Chunk<T, false>& c
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     if (from[i] < C) S[n][2 * i + j] = NAN;
-                    if (n < 2 && 8 * n + 2 * q + j >= from[i]) Y[n & 1][2 * i + j] = NAN;
+                    if (n < 2 && 8 * n + 2 * q + j >= from[i]) Y.c[n & 1][2 * i + j] = NAN;
                 }
         }
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[8 * n + 2 * q + (j & 1)][g + 8 * (j >> 1)] = Y[n][j];
+        for (int j = 0; j < 4; ++j) y[8 * n + 2 * q + (j & 1)][g + 8 * (j >> 1)] = Y.c[n][j];
 }
 
 // The formula as it is written, for chunks with values that are not finite.
@@ -470,33 +480,39 @@ __device__ __forceinline__ void backward_chunk(State& G, const Chunk<T, true>& c
         G[n][2] *= w.x;
         G[n][3] *= w.y;
     }
-    float X[4][4];                           // as two sums
-#pragma unroll
-    for (int n = 0; n < 4; ++n) zero(X[n]);
+    Sums<2> X;
+    X.clear();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {            // X = G B'^T
         const float4 b[2] = {along(&ch.a[g][8 * k + 2 * q]), along(&ch.a[8 + g][8 * k + 2 * q])};
-        products<2>(X + (k & 1 ? 2 : 0), rows_of(G[k][0], G[k][1], G[k][2], G[k][3]), b);
+        products(X, rows_of(G[k][0], G[k][1], G[k][2], G[k][3]), b);
+    }
+    X.fold();
+    Rows x[2], v[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        x[s] = rows_of(X.c[s][0], X.c[s][1], X.c[s][2], X.c[s][3]);
+        const T *v0 = &ch.v[8 * s + 2 * q][row + g], *v1 = v0 + kHead + 8;
+        v[s] = rows_of(to_f32(v0[0]), to_f32(v1[0]), to_f32(v0[8]), to_f32(v1[8]));
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < 8; n += 4) {         // G += X A + dY^T R'
+        Sums<4> d;
+        d.clear();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) X[n][j] += X[n + 2][j];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {            // G += X A + dY^T R'
-        const Rows x = rows_of(X[s][0], X[s][1], X[s][2], X[s][3]);
-        const T *v0 = &ch.v[8 * s + 2 * q][row + g], *v1 = v0 + kHead + 8;
-        const Rows v = rows_of(to_f32(v0[0]), to_f32(v1[0]), to_f32(v0[8]), to_f32(v1[8]));
-#pragma unroll
-        for (int n = 0; n < 8; n += 4) {
+        for (int s = 0; s < 2; ++s) {
             float4 b[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) b[i] = down(&ch.b[8 * s + 2 * q][8 * (n + i) + g], LB);
-            products<4>(G + n, x, b);
+            products(d, x[s], b);
 #pragma unroll
             for (int i = 0; i < 4; ++i) b[i] = down(&ch.k[8 * s + 2 * q][8 * (n + i) + g], LB);
-            products<4, sizeof(T) == 2>(G + n, v, b);
+            products<sizeof(T) == 2>(d, v[s], b);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) G[n + i][j] += d.at(i, j);
     }
 }
 

@@ -46,14 +46,10 @@ __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast
 
 // Half of a [16, 64] result per warp: four products of 8 columns, c[n] the
 // columns 32 half + 8 n.
-using Half = float[4][4];
+using Half = Sums<4>;
 struct Lane {
     int g, q, first;                         // first: 32 half
 };
-__device__ __forceinline__ void clear(Half& c) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n) zero(c[n]);
-}
 // c += X Y^T, X [16, 64], Y [64, 64]
 __device__ __forceinline__ void times_rows(Half& c, const Lane& l, const float (*X)[LD], const float (*Y)[LD]) {
 #pragma unroll 2
@@ -61,7 +57,7 @@ __device__ __forceinline__ void times_rows(Half& c, const Lane& l, const float (
         float4 b[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) b[n] = along(&Y[l.first + 8 * n + l.g][k + 2 * l.q]);
-        products<4>(c, rows_at(X, l.g, k + 2 * l.q), b);
+        products(c, rows_at(X, l.g, k + 2 * l.q), b);
     }
 }
 // c += X Y, X [16, N] (or, TRANSPOSED, of X [N, 16] the columns), Y [N, 64]
@@ -72,38 +68,34 @@ __device__ __forceinline__ void times(Half& c, const Lane& l, const float (*X)[L
         float4 b[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) b[n] = down(&Y[k + 2 * l.q][l.first + 8 * n + l.g], LD);
-        products<4>(c, TRANSPOSED ? columns_at(X, l.g, k + 2 * l.q) : rows_at(X, l.g, k + 2 * l.q), b);
+        products(c, TRANSPOSED ? columns_at(X, l.g, k + 2 * l.q) : rows_at(X, l.g, k + 2 * l.q), b);
     }
 }
 // m = X Y^T, both [16, 64], what lies above the diagonal (or on it, STRICT) zero
 __device__ __forceinline__ void square(float (*m)[LM], const Lane& l, const float (*X)[LD], const float (*Y)[LD],
                                        bool strict) {
-    float c[4][4];                           // two column halves, each as two sums
-#pragma unroll
-    for (int n = 0; n < 4; ++n) zero(c[n]);
+    Sums<2> c;                               // two column halves
+    c.clear();
 #pragma unroll 2
-    for (int k = 0; k < kHead; k += 16) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = k + 8 * i + 2 * l.q;
-            const float4 b[2] = {along(&Y[l.g][at]), along(&Y[8 + l.g][at])};
-            products<2>(c + 2 * i, rows_at(X, l.g, at), b);
-        }
+    for (int k = 0; k < kHead; k += 8) {
+        const int at = k + 2 * l.q;
+        const float4 b[2] = {along(&Y[l.g][at]), along(&Y[8 + l.g][at])};
+        products(c, rows_at(X, l.g, at), b);
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int t = l.g + 8 * (j >> 1), s = 8 * n + 2 * l.q + (j & 1);
-            m[t][s] = t > s || (t == s && !strict) ? c[n][j] + c[n + 2][j] : 0.f;
+            m[t][s] = t > s || (t == s && !strict) ? c.at(n, j) : 0.f;
         }
 }
 __device__ __forceinline__ void put(const Half& c, const Lane& l, float (*to)[LD]) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
         const int k = l.first + 8 * n + 2 * l.q;
-        *reinterpret_cast<float2*>(&to[l.g][k]) = make_float2(c[n][0], c[n][1]);
-        *reinterpret_cast<float2*>(&to[l.g + 8][k]) = make_float2(c[n][2], c[n][3]);
+        *reinterpret_cast<float2*>(&to[l.g][k]) = make_float2(c.at(n, 0), c.at(n, 1));
+        *reinterpret_cast<float2*>(&to[l.g + 8][k]) = make_float2(c.at(n, 2), c.at(n, 3));
     }
 }
 // sum over the 16 tokens of c times X, into z
@@ -113,7 +105,7 @@ __device__ __forceinline__ void weigh(const Half& c, const Lane& l, const float 
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int k = l.first + 8 * n + 2 * l.q + j;
-            float s = fmaf(c[n][j], X[l.g][k], c[n][j + 2] * X[l.g + 8][k]);
+            float s = fmaf(c.at(n, j), X[l.g][k], c.at(n, j + 2) * X[l.g + 8][k]);
             s += __shfl_xor_sync(0xffffffffu, s, 4);
             s += __shfl_xor_sync(0xffffffffu, s, 8);
             s += __shfl_xor_sync(0xffffffffu, s, 16);
@@ -194,7 +186,7 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
     const int warp = tid >> 5, lane = tid & 31, pair = warp >> 1;
     const Lane l = {lane >> 2, lane & 3, 32 * (warp & 1)};
     Half acc;
-    clear(acc);
+    acc.clear();
     if (warp == 0) square(sm.ab, l, sm.A, sm.B, true);
     else if (warp == 1) square(sm.ak, l, sm.A, sm.K, true);
     else if (warp == 2) square(sm.rb, l, sm.R, sm.B, false);
@@ -255,7 +247,7 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
     __syncthreads();
 
     // ---- the parts that need no more 16 x 16 products, and those products
-    if (pair < 2) clear(acc);
+    if (pair < 2) acc.clear();
     if (pair == 0) times<kHead, false>(acc, l, sm.E, sm.S0);             // dA
     else if (pair == 1) {                                                // dB
         times<kHead, false>(acc, l, sm.U, sm.G);
@@ -263,7 +255,10 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
     } else if (warp == 4) square(sm.yu, l, sm.dY, sm.U, false);
     else if (warp == 5) square(sm.eu, l, sm.E, sm.U, true);
     else if (warp == 6) square(sm.ev, l, sm.E, sm.V, true);
-    if (pair == 2) times<C, true>(acc, l, sm.ak, sm.E);                  // dV
+    if (pair == 2) {                                                     // dV
+        times<C, true>(acc, l, sm.ak, sm.E);
+        acc.fold();
+    }
     __syncthreads();
     Half more;                                                           // dK, of the pair that has dV
     if (pair == 0) {
@@ -273,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
         times<C, true>(acc, l, sm.yu, sm.R);
         times<C, true>(acc, l, sm.eu, sm.A);
     } else if (pair == 2) {
-        clear(more);
+        more.clear();
         times<kHead, false>(more, l, sm.V, sm.G);
         weigh(more, l, sm.K, sm.z[2]);
         times<C, true>(more, l, sm.yv, sm.R);
