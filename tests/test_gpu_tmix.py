@@ -134,6 +134,52 @@ def test_scan_and_gradients(starts, H, wide, dtype):
         assert torch.all(x[outside] == 7.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("H,lens", [(1, [(7 * i) % 50 for i in range(70)]), (66, [1, 0, 15, 16, 17, 50]),
+                                    (40, [33, 31, 130])], ids=["70x1", "6x66", "3x40"])
+def test_many_heads(H, lens, dtype):
+    """Enough heads of all sequences together for the kernel on the tensor cores (more than 64), 40 per launch too."""
+    starts = np.cumsum([0] + lens).tolist()
+    T, S = starts[-1], len(lens)
+    xs = inputs(T, H, dtype, seed=T + H, wide=H == 40)
+    g = torch.Generator().manual_seed(T)
+    state = (0.3 * torch.randn((S, H, HEAD, HEAD), generator=g)).cuda()
+    dstate = (0.1 * torch.randn((S, H, HEAD, HEAD), generator=g)).cuda()
+    dy = torch.randn((T, H, HEAD), generator=g).to(dtype).cuda()
+    seq = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    ckpt = rq.tmix_ckpt(xs[0], S)
+    out, end = rq.tmix_scan(*xs, seq, state=state, ckpt=ckpt)
+    got, dstart = rq.tmix_scan_bwd(*xs, seq, ckpt, dy, dstate_out=dstate)
+    ref_y, ref_S, ref_g, ref_G = reference(xs, starts, state, dy, dstate)
+    check(out, ref_y, "y")
+    check(end, ref_S, "state")
+    for n, x, ref in zip("rdkvab", got, ref_g):
+        check(x, ref, "d" + n, times=2.0 if n == "d" else 1.0)
+    check(dstart, ref_G, "dstate")
+    again, end2 = rq.tmix_scan(*xs, seq, state=state)
+    assert torch.equal(out, again) and torch.equal(end, end2)
+
+
+@pytest.mark.parametrize("name", ["r", "d", "k", "v", "a", "b"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 3e38])
+@pytest.mark.parametrize("H", [2, 66])
+def test_non_finite_and_huge_inputs_reach_no_earlier_token(name, value, H):
+    """One element at token 21: the tokens before it, the other heads and the other sequence keep their values (the
+    head's own chunk may be taken another way: within the tolerance)."""
+    starts = [0, 40, 60]
+    xs = inputs(60, H, torch.float32, seed=11)
+    seq = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    clean, _ = rq.tmix_scan(*xs, seq)
+    xs["rdkvab".index(name)][21, 1, 9] = value
+    y, end = rq.tmix_scan(*xs, seq)
+    rest = torch.ones(60, H, dtype=torch.bool)
+    rest[:40, 1] = False
+    assert torch.equal(y[rest.cuda()], clean[rest.cuda()])
+    check(y[:21, 1], clean[:21, 1].double().cpu().numpy(), "earlier tokens")
+    if np.isnan(value):
+        assert torch.isnan(y[21, 1, 9] if name == "v" else y[21, 1]).all()
+
+
 def test_scan_without_states():
     starts = [0, 40, 50]
     xs = inputs(50, 2, torch.float32, seed=1)

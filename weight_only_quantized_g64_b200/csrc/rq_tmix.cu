@@ -20,9 +20,10 @@
 // About 204 + 87 MMAs per warp and chunk (rq_tf32.cuh), 8 cycles each, bound the
 // kernel from below (2300 cycles a chunk; the row warps take 2500 alone and 5000
 // beside the preparing ones, which issue twice their instructions).  Plain fp32
-// FMAs over pairs of tokens spent their time on shuffles and on reading each
-// token's vectors for every row: 1.16 ms where this takes 0.79 (8192 tokens of 64
-// heads, the longest sequence 58 % of them).
+// FMAs over pairs of tokens (rq_tmix_pairs.cu, which takes few heads) spend their
+// time on shuffles and on reading each token's vectors for every row: 1.12 ms
+// where this takes 0.80 (8192 tokens of 64 heads, the longest sequence 58 % of
+// them).
 //
 // The products see every token of a chunk at once, so a value that is not finite
 // would reach earlier tokens through a factor of 0.  A chunk with one in r, d, k,
@@ -678,6 +679,13 @@ __global__ void __launch_bounds__(128) tmix_step_kernel(const TmixArgs p) {
 }  // namespace
 
 cudaError_t launch_tmix_scan(const TmixArgs& a, bool half, bool reverse, cudaStream_t s) {
+    // Up to 64 heads of all sequences together leave most of the SMs without one
+    // of this kernel's CTAs, and its first chunk takes 10 us; pairs of tokens split
+    // a head over four or eight CTAs.  Forwards and backwards in us, pairs / this
+    // kernel: 12 heads of 128 tokens 16 + 13 / 27 + 21, of 1024 101 + 81 / 180 +
+    // 150; 32 heads of 512 65 + 49 / 94 + 77; 64 of 512 96 + 78 / 97 + 78; 128 of
+    // 512 188 + 110 / 98 + 79.
+    if (static_cast<int64_t>(a.S) * a.H <= 64) return launch_tmix_pairs(a, half, reverse, s);
     if (half) return reverse ? launch_scan<__half, true>(a, s) : launch_scan<__half, false>(a, s);
     return reverse ? launch_scan<float, true>(a, s) : launch_scan<float, false>(a, s);
 }

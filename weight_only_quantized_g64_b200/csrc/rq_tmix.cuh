@@ -146,6 +146,8 @@ __device__ __forceinline__ int64_t state_of(const TmixArgs& p, int i) {
 // ceil(len / chunk) of them, and lo / chunk + i leaves room for each.
 __device__ __forceinline__ int64_t ckpt_base(int lo, int i) { return lo / kTmixChunk + i; }
 
+// The scan in pairs of tokens (few heads); launch_tmix_scan chooses.
+cudaError_t launch_tmix_pairs(const TmixArgs& a, bool half, bool reverse, cudaStream_t s);
 cudaError_t launch_tmix_scan(const TmixArgs& a, bool half, bool reverse, cudaStream_t s);
 cudaError_t launch_tmix_step(const TmixArgs& a, bool half, cudaStream_t s);
 cudaError_t launch_tmix_chunks_bwd(const TmixArgs& a, bool half, cudaStream_t s);
