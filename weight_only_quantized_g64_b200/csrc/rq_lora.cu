@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(TT) lora_token_kernel(const LoraArgs p) {
     // the first rows of B and y, while the sums are joined.  A warp takes 32 outputs at a time: two MMAs of 16 rows;
     // lane (g, q) supplies rows g and g + 8 of each, and for the ranks that its registers hold the same of t
     constexpr int NR = PR;
-    constexpr int AHEAD = PR <= 4 ? 2 : 1;
+    constexpr int AHEAD = PR <= 2 ? 4 : PR == 4 ? 3 : 1;         // (4 for R = 32 leaves an SM one CTA: 28 us for 13.5)
     const int g = lane >> 2, q = lane & 3;
     const int rank0 = rank_at<PR>(q, 0);
     const uint16_t* bp = p.B + static_cast<int64_t>(a) * p.N * p.R + rank0;
@@ -299,10 +299,11 @@ __device__ __forceinline__ int next_adapter(int id, int after) {
     return __reduce_min_sync(0xffffffffu, id > after ? id : INT_MAX);
 }
 
-// Four consecutive outputs, `left` of them inside the row; `wide`: 4 | N.
-template <typename T>
-__device__ __forceinline__ void get4(const void* p, int64_t at, int64_t left, bool wide, float f[4]) {
-    if (wide && left >= 4) {
+// Four consecutive outputs, `left` of them inside the row; WIDE: 4 | N.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void get4(const void* p, int64_t at, int64_t left, float f[4]) {
+    if constexpr (WIDE) {
+        if (left <= 0) return;
         if constexpr (sizeof(T) == 4) {
             const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
             f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
@@ -312,14 +313,15 @@ __device__ __forceinline__ void get4(const void* p, int64_t at, int64_t left, bo
             const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
             f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = j < left ? get<T>(p, at + j) : 0.f;
+        for (int j = 0; j < 4; ++j) f[j] = j < left ? get<T>(p, at + j) : 0.f;
+    }
 }
-template <typename T>
-__device__ __forceinline__ void put4(void* p, int64_t at, int64_t left, bool wide, const float f[4]) {
-    if (wide && left >= 4) {
+template <typename T, bool WIDE>
+__device__ __forceinline__ void put4(void* p, int64_t at, int64_t left, const float f[4]) {
+    if constexpr (WIDE) {
+        if (left <= 0) return;
         if constexpr (sizeof(T) == 4) {
             *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(f[0], f[1], f[2], f[3]);
         } else {
@@ -327,11 +329,11 @@ __device__ __forceinline__ void put4(void* p, int64_t at, int64_t left, bool wid
             *reinterpret_cast<uint2*>(static_cast<__half*>(p) + at) =
                 make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (j < left) put<T>(p, at + j, f[j]);
+        for (int j = 0; j < 4; ++j)
+            if (j < left) put<T>(p, at + j, f[j]);
+    }
 }
 
 // The workspace: per tile of 16 tokens and MMA step the four registers of every lane, hi then lo; then 2^-e of
@@ -459,11 +461,8 @@ __global__ void __launch_bounds__(SW * 32) lora_sums_kernel(const LoraArgs p) {
 // out = epi(y + t B^T): a warp takes 16 tokens x 64 outputs.  A lane's columns in a pair of 8-column products are four
 // neighbours: column c of product i stands for output 16 (i / 2) + 4 (c / 2) + 2 (i % 2) + c % 2.
 constexpr int EW = 8;                        // warps of a CTA: 4 tiles of tokens x 2 of outputs, which share B and t in L1
-template <typename T, int PR>
-#ifndef VAR_OCC
-#define VAR_OCC (PR <= 4 ? 3 : 2)
-#endif
-__global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const LoraArgs p) {
+template <typename T, int PR, bool WIDE>
+__global__ void __launch_bounds__(EW * 32, 2) lora_outputs_kernel(const LoraArgs p) {
     constexpr int NR = PR, STEPS = mma_steps<PR>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int tiles = (p.M + TM - 1) / TM, tile = blockIdx.y * 4 + (warp & 3), m0 = tile * TM;
@@ -472,7 +471,6 @@ __global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const Lo
     if (n0 >= p.N) return;
     const int id = m0 + (lane & 15) < p.M ? adapter_of(p, m0 + (lane & 15)) : -1;
     const int id_of[2] = {__shfl_sync(0xffffffffu, id, g), __shfl_sync(0xffffffffu, id, g + 8)};
-    const bool wide = (p.N & 3) == 0;
     const int64_t rows[2] = {m0 + g, m0 + g + 8};
     float acc[4][2][4];                      // [16 outputs][row half][neighbour]: y, then the sum
 #pragma unroll
@@ -480,7 +478,7 @@ __global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const Lo
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int64_t n = n0 + 16 * i + 4 * q;
-            if (rows[half] < p.M) get4<T>(p.y, rows[half] * p.N + n, p.N - n, wide, acc[i][half]);
+            if (rows[half] < p.M) get4<T, WIDE>(p.y, rows[half] * p.N + n, p.N - n, acc[i][half]);
         }
     bool waited = false;
     for (int a = next_adapter(id, -1); a != INT_MAX; a = next_adapter(id, a)) {
@@ -490,18 +488,19 @@ __global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const Lo
         constexpr bool HOLD = PR <= 8;       // t stays in registers; else it is read for every 16 outputs
         uint4 held[HOLD ? STEPS : 1][2];
         const uint4* work = p.work + static_cast<int64_t>(tile) * STEPS * 64 + lane;
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {     // 16 outputs
-            uint32_t b[2][NR];
+        constexpr int AHEAD = PR <= 8 ? 1 : 0;   // the rows of the next 16 outputs are on their way (if registers hold them)
+        uint32_t b[1 + AHEAD][2][NR];
+        const auto fetch = [&](int i) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int n = 16 * (i >> 1) + 4 * (g >> 1) + 2 * h + (g & 1);
-                row_of_b<PR>(B + static_cast<int64_t>(n) * p.R, n0 + n < p.N, rank0, rank, b[h]);
-                if (ragged) {
-#pragma unroll
-                    for (int j = 0; j < NR; ++j) b[h][j] &= keep_of(rank_at<PR>(q, j), rank);
-                }
+                const int n = 16 * i + 4 * (g >> 1) + 2 * h + (g & 1);
+                row_of_b<PR>(B + static_cast<int64_t>(n) * p.R, n0 + n < p.N, rank0, rank, b[i & AHEAD][h]);
             }
+        };
+        if (AHEAD) fetch(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {        // 16 outputs
+            if (i + AHEAD < 4) fetch(i + AHEAD);
             if (!waited) {                   // y and the first rows of B are on their way; t comes from the launch before
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 waited = true;
@@ -513,6 +512,12 @@ __global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const Lo
                     held[HOLD ? s : 0][1] = work[s * 64 + 32];
                 }
             }
+            if (ragged) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < NR; ++j) b[i & AHEAD][h][j] &= keep_of(rank_at<PR>(q, j), rank);
+            }
             float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const Lo
                 const uint32_t fh[4] = {hi.x, hi.y, hi.z, hi.w}, fl[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t fb[2] = {b[h][2 * s < NR ? 2 * s : 0], NR > 1 ? b[h][2 * s + 1 < NR ? 2 * s + 1 : 0] : 0u};
+                    const uint32_t fb[2] = {b[i & AHEAD][h][2 * s < NR ? 2 * s : 0], NR > 1 ? b[i & AHEAD][h][2 * s + 1 < NR ? 2 * s + 1 : 0] : 0u};
                     mma(c[h], fl, fb);
                     mma(c[h], fh, fb);
                 }
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const Lo
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float& o = acc[i >> 1][half][2 * h + j];
+                        float& o = acc[i][half][2 * h + j];
                         o = fmaf(c[h][2 * half + j], f, o);
                     }
             }
@@ -550,7 +555,7 @@ __global__ void __launch_bounds__(EW * 32, VAR_OCC) lora_outputs_kernel(const Lo
             if (rows[half] >= p.M) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][half][j] = finish(acc[i][half][j], p.relu_sq);
-            put4<T>(p.out, rows[half] * p.N + n, p.N - n, wide, acc[i][half]);
+            put4<T, WIDE>(p.out, rows[half] * p.N + n, p.N - n, acc[i][half]);
         }
 }
 
@@ -571,7 +576,8 @@ cudaError_t launch_tiles(const LoraArgs& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_outputs_kernel<T, PR>, a);
+    return a.N % 4 == 0 ? cudaLaunchKernelEx(&cfg, lora_outputs_kernel<T, PR, true>, a)
+                        : cudaLaunchKernelEx(&cfg, lora_outputs_kernel<T, PR, false>, a);
 }
 
 template <typename T>
