@@ -337,7 +337,9 @@ rq_status rq_gemm_wq(const uint16_t *x, int64_t M, int64_t K, const void *codes,
  * a token with a negative id has no adapter: out[m, n] = epi(y[m, n]); an id
  * that is not below L counts as none too and sets dev_status (optional,
  * caller-zeroed device int) to RQ_ERR_RANGE.  Sums are fp32 (the products of
- * fp16 values exact, t kept to at least 22 bits); out is rounded once.
+ * fp16 values exact, t kept to 22 bits or, where it is small, to 2^-38 of the
+ * token's largest); out is rounded once.  A value that is not finite reaches
+ * its own token, or (in B) its own column, and no other.
  *
  * x: fp16 [M, K].  A: fp16 [L, R, K].  B: fp16 [L, N, R].  ids: int32 [M].
  * ranks: int32 [L] or NULL (all R); values above R count as R, below 0 as 0;
@@ -346,8 +348,8 @@ rq_status rq_gemm_wq(const uint16_t *x, int64_t M, int64_t K, const void *codes,
  * RQ_OUT_F16); out may be y itself, else they must not overlap.  epilogue:
  * RQ_EPI_NONE or RQ_EPI_RELU_SQ (the squared ReLU then comes here, not in the
  * product before).  Bad dtype or epilogue: RQ_ERR_RANGE.  K % 8 == 0, R % 8 ==
- * 0, 8 <= R <= RQ_MAX_LORA_RANK, 1 <= M <= 4194240, any N >= 1, else
- * RQ_ERR_SHAPE.  work: rq_lora_work_bytes(M, R) bytes, 16-byte aligned (0 bytes,
+ * 0, 8 <= R <= RQ_MAX_LORA_RANK, 1 <= M <= 4194240, 1 <= N < 2^31, K and L at
+ * most 2^30, else RQ_ERR_SHAPE.  work: rq_lora_work_bytes(M, R) bytes, 16-byte aligned (0 bytes,
  * NULL allowed, for M <= RQ_MAX_DECODE_M); two calls that may overlap need two.
  * Tokens of one request need not be neighbours, but neighbours are faster.
  * Deterministic; asynchronous on `stream`; allocates nothing.
@@ -372,8 +374,8 @@ rq_status rq_lora_add(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A
  *
  * y, add, gate: [M, D] of dtype (RQ_OUT_F32 or RQ_OUT_F16), rows ld_* elements
  * apart; h, h_out: [M, D] of the same dtype, contiguous; x: fp16 [M, D].
- * add, gate, h, alpha: NULL when absent.  h_out may be h itself; h_out or x may
- * be NULL, not both.  Norms: RQ_NORM_NONE, RQ_NORM_LAYER ((v - mean) /
+ * add, gate, h, alpha: NULL when absent.  h_out may be h itself, else the outputs
+ * must not overlap the inputs or each other; h_out or x may be NULL, not both.  Norms: RQ_NORM_NONE, RQ_NORM_LAYER ((v - mean) /
  * sqrt(var + eps), var the mean square about the mean), RQ_NORM_RMS (v /
  * sqrt(mean square + eps)), over the whole row or, for post, over post_group
  * channels (0 or D: the row; else 8, 16, .. 256, dividing D), then * weight + bias
@@ -412,13 +414,14 @@ rq_status rq_norm_residual(const void *y, int64_t ld_y, int64_t M, int64_t D, in
  * (RQ_OUT_F32 or RQ_OUT_F16, else RQ_ERR_RANGE), tokens ld elements apart
  * (ld >= 64 H, ld % 8 == 0, else RQ_ERR_SHAPE), so that they may be columns of
  * one larger matrix.  y (and every gradient): [T, H, 64] contiguous, same type,
- * 16-byte aligned.
+ * 16-byte aligned, overlapping no input.
  * seq_start: int32 [S + 1] device: sequence i is the tokens seq_start[i] ..
  * seq_start[i + 1] - 1; a sequence may be empty (its state is passed on).
  * Tokens outside every sequence are not read and their outputs are left as
  * they were.  Offsets must not fall; a pair that falls or leaves 0 .. T sets
  * dev_status (optional, caller-zeroed device int) to RQ_ERR_RANGE and its
- * sequence is skipped.
+ * sequence is skipped (the gradients' call may then leave those of other
+ * sequences unwritten too).
  * state_in: fp32 [*, H, 64, 64] device or NULL (zeros).  state_out: the same,
  * or NULL (dropped); it may be state_in itself.  slots: int32 [S] device or
  * NULL: which state sequence i uses, 0 <= slot < n_slots (n_slots >= 1 states
@@ -427,14 +430,21 @@ rq_status rq_norm_residual(const void *y, int64_t ld_y, int64_t M, int64_t D, in
  * Two sequences of one call must not share a slot when state_out is given.
  * ckpt: NULL, or rq_tmix_ckpt_bytes(T, S, H) bytes for rq_tmix_scan_bwd: the
  * state before every 16th token of each sequence.
- * 0 <= T < 2^30, S >= 1, H >= 1, (T / 16 + S) * H < 2^29, else RQ_ERR_SHAPE.
+ * 0 <= T < 2^30, S >= 1, 1 <= H <= 2^20, (T / 16 + S) * H < 2^29, else
+ * RQ_ERR_SHAPE.
  * With T = 0 the [T, ...] pointers may be NULL.
+ * Values that are not finite: no token before them changes, no other head and
+ * no other sequence, and one in v stays in its row of the state; what they reach
+ * is not finite, but may be NaN where the formula gives an infinity (so may v
+ * from 1e30 on).  A state that itself outgrows fp32 may leave the 15 tokens
+ * before that not finite too.
  *
  * rq_tmix_scan_bwd -- gradients of the same call: dy [T, H, 64] and dstate_out
  * (gradient of the final states, fp32 [S, H, 64, 64], NULL: zeros) give dr ..
  * db and dstate_in (gradient of the initial states, NULL: dropped).  Same
  * inputs as the forward call, with its ckpt.  work: rq_tmix_ckpt_bytes bytes.
- * States are by sequence (no slots).  Deterministic.
+ * States are by sequence (no slots).  Deterministic.  A value that is not finite
+ * may spoil every gradient of its head in the same 16 tokens of its sequence.
  *
  * rq_tmix_step -- one token for each of B sequences: r .. b and y [B, H, 64],
  * states and slots as above.  B >= 1.
