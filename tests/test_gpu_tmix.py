@@ -138,7 +138,7 @@ def test_scan_and_gradients(starts, H, wide, dtype):
 @pytest.mark.parametrize("H,lens", [(1, [(7 * i) % 50 for i in range(70)]), (66, [1, 0, 15, 16, 17, 50]),
                                     (40, [33, 31, 130])], ids=["70x1", "6x66", "3x40"])
 def test_many_heads(H, lens, dtype):
-    """Enough heads of all sequences together for the kernel on the tensor cores (more than 64), 40 per launch too."""
+    """Enough heads of all sequences together for the kernel on the tensor cores; more sequences than it orders, too."""
     starts = np.cumsum([0] + lens).tolist()
     T, S = starts[-1], len(lens)
     xs = inputs(T, H, dtype, seed=T + H, wide=H == 40)
@@ -272,6 +272,23 @@ def test_bad_offsets_and_slots_are_skipped():
     y1, _ = rq.tmix_step(*(x[:1] for x in xs), state=pool, state_out=pool, slots=slots, dev_status=status)
     assert status.item() == rq.ERR_RANGE and torch.all(pool == 5.0)
     check(y1, reference([x[:1] for x in xs], [0, 1], None)[0], "y without a state")
+
+
+def test_bad_offsets_among_many_heads():
+    """The kernel that takes sequences in the order of their lengths: a bad pair changes no other sequence."""
+    T, H = 80, 40
+    xs = inputs(T, H, torch.float16, seed=11)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    seq = torch.tensor([0, 5, 40, 95, 60, 75], dtype=torch.int32, device="cuda")       # (40, 95) and (95, 60) are bad
+    y = torch.full((T, H, HEAD), 7.0, dtype=torch.float16, device="cuda")
+    end = torch.full((5, H, HEAD, HEAD), 5.0, device="cuda")
+    rq.tmix_scan(*xs, seq, state_out=end, y=y, dev_status=status)
+    assert status.item() == rq.ERR_RANGE
+    for i, lo, hi in ((0, 0, 5), (1, 5, 40), (4, 60, 75)):
+        ref_y, ref_S = reference([x[lo:hi] for x in xs], [0, hi - lo], None)
+        check(y[lo:hi], ref_y, "y")
+        check(end[i:i + 1], ref_S, "state")
+    assert torch.all(end[2:4] == 5.0) and torch.all(y[40:60] == 7.0) and torch.all(y[75:] == 7.0)
 
 
 def test_gradients_against_differences():

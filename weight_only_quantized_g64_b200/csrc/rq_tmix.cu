@@ -18,12 +18,15 @@
 // two take 0.79 and three 0.90, which leave less to the row warps).
 //
 // About 204 + 87 MMAs per warp and chunk (rq_tf32.cuh), 8 cycles each, bound the
-// kernel from below (2300 cycles a chunk; the row warps take 2500 alone and 5000
-// beside the preparing ones, which issue twice their instructions).  Plain fp32
-// FMAs over pairs of tokens (rq_tmix_pairs.cu, which takes few heads) spend their
-// time on shuffles and on reading each token's vectors for every row: 1.12 ms
-// where this takes 0.80 (8192 tokens of 64 heads, the longest sequence 58 % of
-// them).
+// kernel from below: 2300 cycles a chunk.  It takes 4700: a row warp's chain of
+// products is 2700 cycles long by itself and 4200 beside two preparing warps on
+// its quarter of the SM, which issue twice its instructions; it waits for them
+// 30 cycles a chunk.  (Two CTAs per head that prepare for one another through
+// distributed shared memory: 4500 cycles with four preparing groups, and more
+// where other heads wait for an SM.)  Plain fp32 FMAs over pairs of tokens
+// (rq_tmix_pairs.cu, which takes few heads) spend their time on shuffles and on
+// reading each token's vectors for every row: 1.12 ms where this takes 0.80 (8192
+// tokens of 64 heads, the longest sequence 58 % of them).
 //
 // The products see every token of a chunk at once, so a value that is not finite
 // would reach earlier tokens through a factor of 0.  A chunk with one in r, d, k,
@@ -517,12 +520,29 @@ __device__ __forceinline__ void backward_chunk(State& G, const Chunk<T, true>& c
     }
 }
 
+// The sequence that is index-th in the order of lengths, the longest first: with
+// more CTAs than SMs the last ones to start are then short (64 heads, sequences of
+// 864, 864, 864, 864 and 4736 tokens: 1050 us in their own order, 770 in this).
+// Of up to 32 sequences, whose lengths a warp holds; more are taken as they come.
+__device__ __forceinline__ int by_length(const TmixArgs& p, int index) {
+    if (p.S > 32) return index;
+    const int lane = threadIdx.x & 31;
+    const int64_t len = lane < p.S ? static_cast<int64_t>(p.seq_start[lane + 1]) - p.seq_start[lane] : 0;
+    const int mine = static_cast<int>(max(int64_t{0}, min(len, p.T)));      // (whatever bad offsets give)
+    int longer = 0;
+    for (int i = 0; i < p.S; ++i) {
+        const int other = __shfl_sync(0xffffffffu, mine, i);
+        longer += other > mine || (other == mine && i < lane);
+    }
+    return __ffs(__ballot_sync(0xffffffffu, lane < p.S && longer == index)) - 1;
+}
+
 // One CTA: one head of one sequence; warps 0..3 hold its rows, the others prepare.
 template <typename T, bool REV>
 __global__ void __launch_bounds__(128 * (1 + GROUPS), 1) tmix_scan_kernel(const TmixArgs p) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem<T, REV>& sm = *reinterpret_cast<Smem<T, REV>*>(smem_raw);
-    const int h = blockIdx.x % p.H, seq = blockIdx.x / p.H;
+    const int h = blockIdx.x % p.H, seq = by_length(p, blockIdx.x / p.H);
     int lo, hi;
     if (!sequence_of(p, seq, lo, hi)) return;
     const int64_t slot = state_of(p, seq);
@@ -679,13 +699,13 @@ __global__ void __launch_bounds__(128) tmix_step_kernel(const TmixArgs p) {
 }  // namespace
 
 cudaError_t launch_tmix_scan(const TmixArgs& a, bool half, bool reverse, cudaStream_t s) {
-    // Up to 64 heads of all sequences together leave most of the SMs without one
-    // of this kernel's CTAs, and its first chunk takes 10 us; pairs of tokens split
-    // a head over four or eight CTAs.  Forwards and backwards in us, pairs / this
-    // kernel: 12 heads of 128 tokens 16 + 13 / 27 + 21, of 1024 101 + 81 / 180 +
-    // 150; 32 heads of 512 65 + 49 / 94 + 77; 64 of 512 96 + 78 / 97 + 78; 128 of
-    // 512 188 + 110 / 98 + 79.
-    if (static_cast<int64_t>(a.S) * a.H <= 64) return launch_tmix_pairs(a, half, reverse, s);
+    // Up to a head (of all sequences together) for every four SMs, most SMs would be
+    // without one of this kernel's CTAs, and its first chunk takes 10 us; pairs of
+    // tokens split a head over four or eight CTAs.  Forwards + backwards in us, pairs /
+    // this kernel: 12 heads of 128 tokens 16 + 13 / 27 + 21, of 1024 101 + 81 / 180 +
+    // 150; 32 heads of 512 65 + 49 / 94 + 77; 64 of 512 96 + 78 / 97 + 78, of 1024
+    // (forwards) 185 / 173; 128 of 512 188 + 110 / 98 + 79.
+    if (static_cast<int64_t>(a.S) * a.H * 4 <= num_sms()) return launch_tmix_pairs(a, half, reverse, s);
     if (half) return reverse ? launch_scan<__half, true>(a, s) : launch_scan<__half, false>(a, s);
     return reverse ? launch_scan<float, true>(a, s) : launch_scan<float, false>(a, s);
 }
