@@ -128,7 +128,7 @@ constexpr int TT = 256;                      // threads
 
 // PR: pieces of 8 ranks (R <= 8 PR); a row of B is read by PR lanes.
 template <typename T, int PR>
-__global__ void __launch_bounds__(TT) lora_token_kernel(const LoraArgs p) {
+__global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(TT) lora_token_kernel(const LoraArgs p) {
     __shared__ float part[CS][PR * 8];
     __shared__ float ts[PR * 8];
     cg::cluster_group cluster = cg::this_cluster();
@@ -276,18 +276,8 @@ __global__ void __launch_bounds__(TT) lora_token_kernel(const LoraArgs p) {
 
 template <typename T, int PR>
 cudaError_t launch_tokens(const LoraArgs& a, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.M * CS);
-    cfg.blockDim = dim3(TT);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CS;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_token_kernel<T, PR>, a);
+    lora_token_kernel<T, PR><<<a.M * CS, TT, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 // ------------------------------------------------------------ many tokens --
