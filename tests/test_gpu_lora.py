@@ -85,6 +85,16 @@ def test_sizes(M, K, N, R, dtype):
     assert torch.equal(mine, rq.lora_add(x, A, B, ids, y, scale=scale))
 
 
+@pytest.mark.parametrize("M", [90, 1300, 2500])
+def test_many_adapters_in_a_tile(M):
+    """16 tokens of up to 16 adapters, whichever number of CTAs they are dealt over; the number changes no bit."""
+    x, A, B, ids, y, scale = adapters(M, 64, 24, 8, 20, torch.float32, seed=M)
+    out = rq.lora_add(x, A, B, ids, y, scale=scale)
+    check(out, x, A, B, ids, y, scale, what="out")
+    few = rq.lora_add(x[:80], A, B, ids[:80], y[:80], scale=scale)
+    assert torch.equal(few, out[:80])
+
+
 @pytest.mark.parametrize("M", [1, 7, 32, 33, 150])
 def test_ranks_and_what_lies_behind_them(M):
     """Ranks of 0, odd, full, out of range; NaN behind a rank and in adapters that no token uses."""

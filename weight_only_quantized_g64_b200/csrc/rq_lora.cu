@@ -15,15 +15,17 @@
 // way before the cluster meets.  Bound by latency: two dependent reads of memory
 // and a barrier.
 //
-// Many tokens (prefill): two launches.  A CTA per 16 tokens splits K over its
-// warps for A x and leaves hi and lo of t in the order of the MMA's registers;
-// then every warp of a second launch takes 16 tokens x 64 outputs without shared
-// memory or barriers, its y and B on their way before the first launch has
-// ended.  Bound by the bytes of x, y and out.  Tokens of several adapters in a
-// warp's 16 are taken in turn, and each keeps its own sum.
+// Many tokens (prefill): two launches.  A CTA per 16 tokens (and some of their
+// adapters) splits K over its warps for A x, 640 KB through its L1 (the bound: 64
+// bytes of every row and load), and leaves hi and lo of t in the order of the
+// MMA's registers; then every warp of a second launch takes 16 tokens x 64 outputs
+// without shared memory or barriers, its y and B on their way before the first
+// launch has ended.  Tokens of several adapters in a warp's 16 are taken in turn, and each
+// keeps its own sum.  2048 tokens beside 4096 x 4096, R = 64: 33 us.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 
@@ -349,7 +351,12 @@ __global__ void __launch_bounds__(SW * 32) lora_sums_kernel(const LoraArgs p) {
     const int s0 = static_cast<int64_t>(steps) * warp / SW, s1 = static_cast<int64_t>(steps) * (warp + 1) / SW;
     const int64_t xrow[2] = {static_cast<int64_t>(min(m0 + g, p.M - 1)) * p.K, static_cast<int64_t>(min(m0 + g + 8, p.M - 1)) * p.K};
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    int slot = blockIdx.y;                   // adapters until the next that is this CTA's
+    bool mine = false;                       // token `row` has one of them
     for (int a = next_adapter(id, -1); a != INT_MAX; a = next_adapter(id, a)) {
+        if (slot-- != 0) continue;
+        slot = gridDim.y - 1;
+        mine = mine || id == a;
         const uint16_t* A = p.A + (static_cast<int64_t>(a) * p.R + g) * p.K;
         float acc[PR][4];
 #pragma unroll
@@ -405,12 +412,14 @@ __global__ void __launch_bounds__(SW * 32) lora_sums_kernel(const LoraArgs p) {
             }
         }
     }
+    const uint32_t tokens = __ballot_sync(0xffffffffu, mine);    // (the same in every warp)
+    if (tokens == 0) return;
     __syncthreads();
     // one warp per token: t in part[0], its scale
-    {
+    if (tokens >> warp & 1) {
         const int a = __shfl_sync(0xffffffffu, id, warp);
-        const int rank = a >= 0 ? rank_of(p, a) : 0;
-        const float s = a >= 0 && p.scale != nullptr ? p.scale[a] : 1.f;
+        const int rank = rank_of(p, a);
+        const float s = p.scale != nullptr ? p.scale[a] : 1.f;
         float top = 0.f;
         for (int r = lane; r < PR * 8; r += 32) {
             float t = 0.f;
@@ -428,23 +437,31 @@ __global__ void __launch_bounds__(SW * 32) lora_sums_kernel(const LoraArgs p) {
         const int e = scale_of(top);
         __syncwarp();
         for (int r = lane; r < PR * 8; r += 32) part[0][warp][r] *= pow2(e);
-        if (lane == 0) {
-            if (m0 + warp < p.M)
-                reinterpret_cast<float*>(p.work + static_cast<int64_t>(gridDim.x) * mma_steps<PR>() * 64)[m0 + warp] = pow2(-e);
-        }
+        if (lane == 0)
+            reinterpret_cast<float*>(p.work + static_cast<int64_t>(gridDim.x) * mma_steps<PR>() * 64)[m0 + warp] = pow2(-e);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < mma_steps<PR>() * 64; i += SW * 32) {
         const int l = i & 31, lo = (i >> 5) & 1, step = i >> 6, gg = l >> 2, qq = l & 3;
+        uint4* const to = p.work + (static_cast<int64_t>(blockIdx.x) * mma_steps<PR>() + step) * 64 + lo * 32 + l;
         uint32_t f[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {        // registers: rows gg, gg + 8 of the first two ranks, then of the next
-            const int r = rank_at<PR>(qq, 2 * step + (j >> 1));
-            const float* t = part[0][gg + 8 * (j & 1)];
-            const __half2 v = r < PR * 8 ? __halves2half2(split(t[r], lo), split(t[r + 1], lo)) : __floats2half2_rn(0.f, 0.f);
+            const int r = rank_at<PR>(qq, 2 * step + (j >> 1)), t = gg + 8 * (j & 1);
+            const __half2 v = r < PR * 8 ? __halves2half2(split(part[0][t][r], lo), split(part[0][t][r + 1], lo))
+                                         : __floats2half2_rn(0.f, 0.f);
             f[j] = *reinterpret_cast<const uint32_t*>(&v);
         }
-        p.work[(static_cast<int64_t>(blockIdx.x) * mma_steps<PR>() + step) * 64 + lo * 32 + l] = make_uint4(f[0], f[1], f[2], f[3]);
+        const bool low = tokens >> gg & 1, high = tokens >> (gg + 8) & 1;
+        if (low && high) {
+            *to = make_uint4(f[0], f[1], f[2], f[3]);
+        } else if (low) {                    // (the other token is another CTA's, or has no adapter)
+            to->x = f[0];
+            to->z = f[2];
+        } else if (high) {
+            to->y = f[1];
+            to->w = f[3];
+        }
     }
 }
 
@@ -555,7 +572,12 @@ cudaError_t launch_tiles(const LoraArgs& a, cudaStream_t s) {
     cudaError_t e = allow_smem<lora_sums_kernel<PR>>(smem);
     if (e != cudaSuccess) return e;
     const int tiles = (a.M + TM - 1) / TM;
-    lora_sums_kernel<PR><<<tiles, SW * 32, smem, s>>>(a);
+    // A tile's adapters are dealt over up to 16 CTAs, as far as two CTAs an SM go: where one request ends and the next
+    // begins the two are then not summed one after the other (2048 tokens of 6 requests, R = 64: 32.9 us, by one CTA
+    // 37.9; 40 tokens of as many requests, R = 16, 4096 x 4096: 16.0, by one 45).  Without a use for them the others cost
+    // their start (8192 tokens of one request beside 2048 x 2048, R = 32: four CTAs a tile 67 us, one 61).
+    const int share = std::max(1, std::min(std::min(a.L, TM), 2 * num_sms() / tiles));
+    lora_sums_kernel<PR><<<dim3(tiles, share), SW * 32, smem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.N + 127) / 128), (tiles + 3) / 4);
