@@ -21,7 +21,7 @@
 // MMA's registers; then every warp of a second launch takes 16 tokens x 64 outputs
 // without shared memory or barriers, its y and B on their way before the first
 // launch has ended.  Tokens of several adapters in a warp's 16 are taken in turn, and each
-// keeps its own sum.  2048 tokens beside 4096 x 4096, R = 64: 33 us.
+// keeps its own sum.  2048 tokens beside 4096 x 4096, R = 64: 32 us.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(SW * 32) lora_sums_kernel(const LoraArgs p) {
                 mma(acc[n], f1, b1);
             }
         };
-        constexpr int DEEP = PR <= 4 ? 4 : PR <= 8 ? 2 : 1;      // steps in flight
+        // steps in flight of a warp; with 16 warps one is enough when it is 160 bytes a lane (8192 tokens, R = 32: four 61
+        // us, two 56; 2048 tokens, R = 64: two 32.9, one 32.0)
+        constexpr int DEEP = PR <= 2 ? 4 : PR == 4 ? 2 : 1;
         Step ring[DEEP];
 #pragma unroll
         for (int i = 0; i < DEEP; ++i)
@@ -573,9 +575,9 @@ cudaError_t launch_tiles(const LoraArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int tiles = (a.M + TM - 1) / TM;
     // A tile's adapters are dealt over up to 16 CTAs, as far as two CTAs an SM go: where one request ends and the next
-    // begins the two are then not summed one after the other (2048 tokens of 6 requests, R = 64: 32.9 us, by one CTA
+    // begins the two are then not summed one after the other (2048 tokens of 6 requests, R = 64: 32.0 us, by one CTA
     // 37.9; 40 tokens of as many requests, R = 16, 4096 x 4096: 16.0, by one 45).  Without a use for them the others cost
-    // their start (8192 tokens of one request beside 2048 x 2048, R = 32: four CTAs a tile 67 us, one 61).
+    // their start (8192 tokens of one request beside 2048 x 2048: four CTAs a tile 8 us more).
     const int share = std::max(1, std::min(std::min(a.L, TM), 2 * num_sms() / tiles));
     lora_sums_kernel<PR><<<dim3(tiles, share), SW * 32, smem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
