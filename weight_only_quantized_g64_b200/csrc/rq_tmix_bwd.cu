@@ -21,7 +21,7 @@
 // About 800 000 multiplications per chunk and head, on the tensor cores
 // (rq_tf32.cuh): 2300 MMAs of 8 cycles over the four of an SM bound it.  With
 // plain FMAs the kernel was bound by shared-memory reads at 4 x 4 results per
-// thread: 322 us where this takes 224 (2048 tokens, 32 heads, fp16).
+// thread: 322 us where this takes 205 (2048 tokens, 32 heads, fp16).
 // A value that is not finite may spoil the gradients of its chunk of 16 tokens.
 #include "rq_tf32.cuh"
 #include "rq_tmix.cuh"
@@ -42,6 +42,13 @@ struct alignas(16) Smem {
     float z[3][kHead];                       // the parts of Z: S0, U^T B, V^T K
 };
 
+__device__ __forceinline__ void cp16(float* dst, const float* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 // Half of a [16, 64] result per warp: four products of 8 columns, c[n] the
@@ -120,6 +127,14 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
     const int tid = threadIdx.x;
     const int h = blockIdx.x % p.H, place = blockIdx.x / p.H;
 
+    // the stored states (every place has memory, whether a chunk uses it or not), on their way while the rest is found
+    const int64_t state = (static_cast<int64_t>(place) * p.H + h) * kHead * kHead;
+    for (int i = tid; i < kHead * kHead / 4; i += THREADS) {
+        const int r = i >> 4, c = (i & 15) * 4;
+        cp16(&sm.S0[r][c], p.ckpt + state + 4 * i);
+        cp16(&sm.G[r][c], p.gckpt + state + 4 * i);
+    }
+
     // the sequence whose stored states hold this place: the last one whose first is not behind it
     int a = 0, b = p.S - 1;
     while (a < b) {
@@ -128,19 +143,16 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
         else b = m - 1;
     }
     int lo, hi;
-    if (!sequence_of(p, a, lo, hi)) return;
+    const bool whole = sequence_of(p, a, lo, hi);
     const int64_t first = ckpt_base(lo, a);
-    if (place < first || place - first >= (hi - lo + C - 1) / C) return;
+    if (!whole || place < first || place - first >= (hi - lo + C - 1) / C) {
+        cp_wait();
+        return;
+    }
     const int64_t t0 = lo + (place - first) * C;
     const int nt = static_cast<int>(min(static_cast<int64_t>(C), hi - t0));
 
     // ---- load
-    const int64_t state = (static_cast<int64_t>(place) * p.H + h) * kHead * kHead;
-    for (int i = tid; i < kHead * kHead / 4; i += THREADS) {
-        const int r = i >> 4, c = (i & 15) * 4;
-        *reinterpret_cast<float4*>(&sm.S0[r][c]) = ld4(p.ckpt + state + 4 * i);
-        *reinterpret_cast<float4*>(&sm.G[r][c]) = ld4(p.gckpt + state + 4 * i);
-    }
     const int et = tid >> 4, ec = (tid & 15) * 4;        // this thread's 4 elements of every [16, 64] array
     const int64_t in_at = (t0 + et) * p.ld + static_cast<int64_t>(h) * kHead + ec;
     const int64_t out_at = ((t0 + et) * p.H + h) * kHead + ec;
@@ -174,7 +186,8 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
         row4(sm.A, mul(xa, wp));
         row4(sm.B, mul(xb, iw));
         row4(sm.K, mul(xk, iw));
-        for (int i = tid; i < kHead * kHead / 4; i += THREADS) {
+        cp_wait();
+        for (int i = tid; i < kHead * kHead / 4; i += THREADS) {             // (what this thread has brought)
             const int r = i >> 4, c = (i & 15) * 4;
             float4* g = reinterpret_cast<float4*>(&sm.G[r][c]);
             *g = mul(*g, ld4(&sm.W[C - 1][c]));
@@ -205,7 +218,9 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
     }
     __syncthreads();
 
-    // ---- right-hand sides; each pair of warps takes one [16, 64] result
+    // ---- right-hand sides; each pair of warps takes one [16, 64] result, the last begins dK beside dR
+    Half more;
+    more.clear();
     if (pair == 0) {
         times_rows(acc, l, sm.A, sm.S0);
         times<C, false>(acc, l, sm.ak, sm.V);
@@ -219,6 +234,10 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
         times<C, true>(acc, l, sm.rk, sm.dY);
     } else {
         times<C, false>(acc, l, sm.yv, sm.K);            // dR: all but its part with U
+        acc.fold();
+        times<kHead, false>(more, l, sm.V, sm.G);
+        weigh(more, l, sm.K, sm.z[2]);
+        more.fold();
     }
     __syncthreads();
 
@@ -260,27 +279,22 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
         acc.fold();
     }
     __syncthreads();
-    Half more;                                                           // dK, of the pair that has dV
     if (pair == 0) {
         times<C, false>(acc, l, sm.eu, sm.B);
         times<C, false>(acc, l, sm.ev, sm.K);
     } else if (pair == 1) {
         times<C, true>(acc, l, sm.yu, sm.R);
         times<C, true>(acc, l, sm.eu, sm.A);
-    } else if (pair == 2) {
-        more.clear();
-        times<kHead, false>(more, l, sm.V, sm.G);
-        weigh(more, l, sm.K, sm.z[2]);
+    } else if (pair == 3) {
+        times<C, false>(acc, l, sm.yu, sm.B);
         times<C, true>(more, l, sm.yv, sm.R);
         times<C, true>(more, l, sm.ev, sm.A);
-    } else {
-        times<C, false>(acc, l, sm.yu, sm.B);
     }
     __syncthreads();                                     // S0 and G are free from here
     float (*dA)[LD] = &sm.S0[0], (*dB)[LD] = &sm.S0[16], (*dV)[LD] = &sm.S0[32], (*dR)[LD] = &sm.S0[48];
     float (*dK)[LD] = &sm.G[0], (*dl)[LD] = &sm.G[16];
     put(acc, l, pair == 0 ? dA : pair == 1 ? dB : pair == 2 ? dV : dR);
-    if (pair == 2) put(more, l, dK);
+    if (pair == 3) put(more, l, dK);
     __syncthreads();
 
     // ---- out, and what each token adds to the decay's gradient
