@@ -221,7 +221,7 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
         const int lz = REV ? LA : LB;
         Sums<2> c;                           // two column halves
         c.clear();
-#pragma unroll 4
+#pragma unroll 2                             // (4: backward walks 4 % slower, for the instruction cache)
         for (int k = 0; k < kHead; k += 8) {
             const float* row = x + g * lx + k + 2 * q;
             const float2 u = *reinterpret_cast<const float2*>(row), v = *reinterpret_cast<const float2*>(row + 8 * lx);

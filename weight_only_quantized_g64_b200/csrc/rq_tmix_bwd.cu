@@ -21,7 +21,9 @@
 // About 800 000 multiplications per chunk and head, on the tensor cores
 // (rq_tf32.cuh): 2300 MMAs of 8 cycles over the four of an SM bound it.  With
 // plain FMAs the kernel was bound by shared-memory reads at 4 x 4 results per
-// thread: 322 us where this takes 205 (2048 tokens, 32 heads, fp16).
+// thread: 322 us where this takes 200 (2048 tokens, 32 heads, fp16).
+// The loops over the summed index are not unrolled: the code of all products is
+// what the instruction cache holds least of (steps of 2 together 205 us, all 268).
 // A value that is not finite may spoil the gradients of its chunk of 16 tokens.
 #include "rq_tf32.cuh"
 #include "rq_tmix.cuh"
@@ -59,7 +61,7 @@ struct Lane {
 };
 // c += X Y^T, X [16, 64], Y [64, 64]
 __device__ __forceinline__ void times_rows(Half& c, const Lane& l, const float (*X)[LD], const float (*Y)[LD]) {
-#pragma unroll 2
+#pragma unroll 1
     for (int k = 0; k < kHead; k += 8) {
         float4 b[4];
 #pragma unroll
@@ -70,7 +72,7 @@ __device__ __forceinline__ void times_rows(Half& c, const Lane& l, const float (
 // c += X Y, X [16, N] (or, TRANSPOSED, of X [N, 16] the columns), Y [N, 64]
 template <int N, bool TRANSPOSED, int LX>
 __device__ __forceinline__ void times(Half& c, const Lane& l, const float (*X)[LX], const float (*Y)[LD]) {
-#pragma unroll 2
+#pragma unroll 1
     for (int k = 0; k < N; k += 8) {
         float4 b[4];
 #pragma unroll
@@ -83,7 +85,7 @@ __device__ __forceinline__ void square(float (*m)[LM], const Lane& l, const floa
                                        bool strict) {
     Sums<2> c;                               // two column halves
     c.clear();
-#pragma unroll 2
+#pragma unroll 1
     for (int k = 0; k < kHead; k += 8) {
         const int at = k + 2 * l.q;
         const float4 b[2] = {along(&Y[l.g][at]), along(&Y[8 + l.g][at])};
