@@ -14,19 +14,19 @@
 // also their first operand once the summed index is taken in the order 2q, 2q+1
 // instead of q, q+4.  Two groups of four warps prepare A', R', B, K', M' of the
 // chunks ahead in turn (with the same products): one chunk's preparation is a
-// chain of small dependent steps, longer than its use (one group: 1.09 ms where
-// two take 0.79 and three 0.90, which leave less to the row warps).
+// chain of small dependent steps, longer than its use (8192 tokens of 64 heads, the
+// longest sequence 58 % of them: one group 1.09 ms, two 0.80, three 1.01, which
+// leave less to the row warps).
 //
 // About 204 + 87 MMAs per warp and chunk (rq_tf32.cuh), 8 cycles each, bound the
-// kernel from below: 2300 cycles a chunk.  It takes 4700: a row warp's chain of
-// products is 2700 cycles long by itself and 4200 beside two preparing warps on
-// its quarter of the SM, which issue twice its instructions; it waits for them
-// 30 cycles a chunk.  (Two CTAs per head that prepare for one another through
-// distributed shared memory: 4500 cycles with four preparing groups, and more
-// where other heads wait for an SM.)  Plain fp32 FMAs over pairs of tokens
-// (rq_tmix_pairs.cu, which takes few heads) spend their time on shuffles and on
-// reading each token's vectors for every row: 1.12 ms where this takes 0.80 (8192
-// tokens of 64 heads, the longest sequence 58 % of them).
+// kernel from below: 2300 cycles a chunk.  It takes 5000 (64 heads of 1024 tokens:
+// the row warps by themselves 107 us, the preparing warps by themselves 128,
+// together 172): both sides are chains of dependent products and share the issue
+// slots.  (Two CTAs per head that prepare for one another through distributed
+// shared memory: 4500 cycles with four preparing groups, and more where other heads
+// wait for an SM.)  Plain fp32 FMAs over pairs of tokens (rq_tmix_pairs.cu, which
+// takes few heads) spend their time on shuffles and on reading each token's
+// vectors for every row: 1.12 ms for 0.80.
 //
 // The products see every token of a chunk at once, so a value that is not finite
 // would reach earlier tokens through a factor of 0.  A chunk with one in r, d, k,
