@@ -189,3 +189,54 @@ def test_beside_a_quantized_projection(M):
     check(out, x, A, B, ids, y, scale, relu_sq=True)
     ref, budget = oracle.matmul(x.cpu().numpy(), codes, scales, bits)
     assert np.all(np.abs(y.double().cpu().numpy() - ref) <= 2e-3 * budget)
+
+
+@pytest.mark.parametrize("M", [8, 64])
+def test_between_products_with_programmatic_launch(M):
+    """Products that may start while the call before them runs: the same bits as without."""
+    K = 512
+    codes, scales = rq.quantize_g64(synth.weights(K, K, seed=3, device="cuda") * 20, 4)
+    x, A, B, ids, _, scale = adapters(M, K, K, 16, 4, torch.float32, seed=M)
+    product = rq.gemv_wq if M <= 32 else rq.gemm_wq
+
+    def chain():
+        v = x
+        for _ in range(3):
+            y = product(v, codes, scales, K, 4)
+            out = rq.lora_add(v, A, B, ids, y, scale=scale)
+            _, v = rq.norm_residual(out, pre="rms")
+        return out, v
+
+    first = chain()
+    rq.set_pdl(True)
+    try:
+        for _ in range(20):
+            for p, q in zip(first, chain()):
+                assert torch.equal(p, q)
+    finally:
+        rq.set_pdl(False)
+
+
+@pytest.mark.parametrize("M", [20, 200])
+def test_two_at_once(M):
+    """Two calls on two streams, each with its own workspace, give what they give one after the other."""
+    calls = [adapters(M, 2048, 2048, 32, 6, torch.float32, seed=70 + i) for i in range(2)]
+    alone = [rq.lora_add(x, A, B, ids, y, scale=scale) for x, A, B, ids, y, scale in calls]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        got = [rq.lora_add(x, A, B, ids, y, scale=scale, stream=s) for (x, A, B, ids, y, scale), s in zip(calls, sides)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(alone, got))
+
+
+def test_offsets_past_32_bits():
+    """Tokens behind more than 2^31 elements of x."""
+    M, K, last = 33008, 65536, 48
+    x = torch.empty((M, K), dtype=torch.float16, device="cuda")
+    x[M - last:] = torch.randn((last, K), device="cuda").half()
+    _, A, B, ids, y, scale = adapters(last, K, 16, 8, 2, torch.float32, seed=2)
+    none = torch.full((M - last,), -1, dtype=torch.int32, device="cuda")
+    out = rq.lora_add(x, A, B, torch.cat([none, ids]), torch.cat([torch.zeros((M - last, 16), device="cuda"), y]), scale=scale)
+    assert torch.equal(out[M - last:], rq.lora_add(x[M - last:], A, B, ids, y, scale=scale))
+    assert torch.all(out[:M - last] == 0)

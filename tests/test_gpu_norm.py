@@ -184,3 +184,16 @@ def test_stream_capture_and_bits():
     h4, x4 = rq.norm_residual(y, **t, **kw)
     assert torch.equal(h3, h4) and torch.equal(x3, x4)
     del graph
+
+
+def test_offsets_past_32_bits():
+    """Rows behind more than 2^31 elements of a wide matrix."""
+    M, D, ld, last = 33000, 128, 65536, 9
+    big = torch.empty((M, ld), dtype=torch.float16, device="cuda")
+    y = big[:, 64:64 + D]
+    y[:] = 1.0
+    y[M - last:] = torch.randn((last, D), device="cuda").half()
+    h = torch.randn((M, D), device="cuda").half()
+    h1, x1 = rq.norm_residual(y, post="layer", h=h, pre="rms")
+    h2, x2 = rq.norm_residual(y[M - last:].contiguous(), post="layer", h=h[M - last:], pre="rms")
+    assert torch.equal(h1[M - last:], h2) and torch.equal(x1[M - last:], x2)

@@ -357,11 +357,12 @@ def test_same_bits_every_time(dtype):
         assert all(torch.equal(p, q) for p, q in zip(first, now))
 
 
-def test_other_stream_and_capture():
+@pytest.mark.parametrize("H", [2, 40])
+def test_other_stream_and_capture(H):
     """On a stream of its own, and captured and replayed on new values."""
-    xs = inputs(70, 2, torch.float16, seed=4)
+    xs = inputs(70, H, torch.float16, seed=4)
     seq = torch.tensor([0, 30, 70], dtype=torch.int32, device="cuda")
-    dy = torch.randn((70, 2, HEAD), device="cuda").half()
+    dy = torch.randn((70, H, HEAD), device="cuda").half()
     ckpt = rq.tmix_ckpt(xs[0], 2)
     y0, s0 = rq.tmix_scan(*xs, seq, ckpt=ckpt)
     g0, d0 = rq.tmix_scan_bwd(*xs, seq, ckpt, dy)
@@ -377,7 +378,7 @@ def test_other_stream_and_capture():
         ck2 = rq.tmix_ckpt(xs[0], 2)
         y2, s2 = rq.tmix_scan(*xs, seq, ckpt=ck2)
         g2, d2 = rq.tmix_scan_bwd(*xs, seq, ck2, dy)
-    new = inputs(70, 2, torch.float16, seed=40)
+    new = inputs(70, H, torch.float16, seed=40)
     for x, n in zip(xs, new):
         x.copy_(n)
     graph.replay()
@@ -387,3 +388,50 @@ def test_other_stream_and_capture():
     assert torch.equal(y2, y3) and torch.equal(s2, s3) and torch.equal(d2, d3)
     assert all(torch.equal(p, q) for p, q in zip(g2, g3))
     del graph
+
+
+@pytest.mark.parametrize("H", [1, 40])
+def test_two_at_once(H):
+    """Two calls on two streams, each with its own memory, give what they give one after the other."""
+    calls = []
+    for i in range(2):
+        xs = inputs(600, H, torch.float32, seed=60 + i)
+        calls.append((xs, torch.tensor([0, 450, 600], dtype=torch.int32, device="cuda"), rq.tmix_ckpt(xs[0], 2),
+                      torch.randn((600, H, HEAD), device="cuda"), torch.cuda.Stream()))
+
+    def both(streams):
+        got = []
+        for xs, seq, ckpt, dy, side in calls:
+            s = side if streams else None
+            y, end = rq.tmix_scan(*xs, seq, ckpt=ckpt, stream=s)
+            grads, start = rq.tmix_scan_bwd(*xs, seq, ckpt, dy, stream=s)
+            got += [y, end, start, *grads]
+        torch.cuda.synchronize()
+        return got
+
+    torch.cuda.synchronize()
+    for p, q in zip(both(False), both(True)):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("H", [1, 40])
+def test_offsets_past_32_bits(H):
+    """The last tokens of a matrix with more than 2^31 elements before them."""
+    T, last, ld = 33000, 24, 65536
+    big = torch.empty((T, ld), dtype=torch.float16, device="cuda")
+    small = inputs(last, H, torch.float16, seed=9)
+    parts = [big[:, (i + 1) * H * HEAD:(i + 2) * H * HEAD].unflatten(1, (H, HEAD)) for i in range(6)]
+    for p, x in zip(parts, small):
+        p[T - last:] = x
+    seq = torch.tensor([T - last, T], dtype=torch.int32, device="cuda")
+    ckpt = rq.tmix_ckpt(parts[0], 1)
+    dy = torch.ones((T, H, HEAD), dtype=torch.float16, device="cuda")
+    y, end = rq.tmix_scan(*parts, seq, ckpt=ckpt)
+    grads, start = rq.tmix_scan_bwd(*parts, seq, ckpt, dy)
+    own = torch.tensor([0, last], dtype=torch.int32, device="cuda")
+    few = rq.tmix_ckpt(small[0], 1)
+    y1, end1 = rq.tmix_scan(*small, own, ckpt=few)
+    grads1, start1 = rq.tmix_scan_bwd(*small, own, few, dy[:last])
+    assert torch.equal(y[T - last:], y1) and torch.equal(end, end1) and torch.equal(start, start1)
+    for p, q in zip(grads, grads1):
+        assert torch.equal(p[T - last:], q)

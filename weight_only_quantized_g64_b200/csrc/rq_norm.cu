@@ -232,8 +232,8 @@ __device__ __forceinline__ void normed(Piece (&u)[R][V], int pieces, const NormA
     else normed_as<R, V, false>(u, pieces, group, eps, inv_n, w, b, shared);
 }
 
-// Relative error below 2^-20: the hardware's 2^x and 1/x are good to 2^-22 and
-// 2^-23, and x log2(e) is rounded once.
+// Relative error at most (|x| + 6) 2^-24 below 0, and 2^-21 above: the hardware's
+// 2^x and 1/x are good to 2^-22 and 2^-23, and x log2(e) is rounded once.
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t x) {
     float2 t = unpack2(mul2(x, both(-1.4426950408889634f)));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.x));

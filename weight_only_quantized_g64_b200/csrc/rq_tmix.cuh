@@ -96,8 +96,9 @@ __device__ __forceinline__ T from_f32(float v) {
 }
 
 // ------------------------------------------------------------------- decay --
-// sigmoid(d), relative error about 2^-21.5 (the hardware's 2^x and 1/x are good
-// to 2^-22 and 2^-23): it scales log w, so the state's error stays below that.
+// sigmoid(d), relative error at most (|d| + 6) 2^-24 below 0 and 2^-21 above (the
+// hardware's 2^x and 1/x are good to 2^-22 and 2^-23, d log2(e) is rounded once):
+// it scales log w, which is small where that grows.
 __device__ __forceinline__ float decay_gate(float d) {
     float e, s;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d * -1.4426950408889634f));
