@@ -13,7 +13,7 @@
 // after one cluster barrier takes an eighth of the outputs; hi and lo are two of
 // the eight columns of an MMA over 16 rows of B, the first of which are on their
 // way before the cluster meets.  Bound by latency: two dependent reads of memory
-// and a barrier.
+// and a barrier; 32 tokens beside 16384 x 4096, R = 32: 13.0 us, 3.4 TB/s.
 //
 // Many tokens (prefill): two launches.  A CTA per 16 tokens (and some of their
 // adapters) splits K over its warps for A x, 640 KB through its L1 (the bound: 64

@@ -399,7 +399,7 @@ cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
     if (smem > (200 << 10)) return launch_rows<T, 1>(a, s);              // two fp32 rows of four tensors
     const cudaError_t e = allow_smem<norm_rows_kernel<T, R>>(200 << 10);
     if (e != cudaSuccess) return e;
-    const int per_sm = std::max(1, std::min(std::min(1024 / threads, 32), (220 << 10) / (smem + 3072)));
+    const int per_sm = std::max(1, std::min(std::min(1024 / threads, 32), (220 << 10) / (smem + (3 << 10))));
     const int64_t grid = std::min<int64_t>((a.M + R - 1) / R, static_cast<int64_t>(num_sms()) * per_sm);
     norm_rows_kernel<T, R><<<static_cast<unsigned>(grid), threads, smem, s>>>(a);
     return cudaGetLastError();

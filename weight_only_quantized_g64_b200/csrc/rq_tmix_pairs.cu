@@ -13,7 +13,7 @@
 // exponential and a reciprocal per channel) while the others take the current
 // ones.
 // What bounds it: the chain of a pair (two dot products, four shuffles, one
-// update: 330 cycles with one row per lane), and with many rows on an SM the
+// update: 375 cycles with one row per lane), and with many rows on an SM the
 // reads of each pair's nine vectors from shared memory.  rq_tmix.cu says where it
 // is left for the kernel on the tensor cores.
 //
