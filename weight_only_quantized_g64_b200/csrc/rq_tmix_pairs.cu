@@ -8,14 +8,15 @@
 //   x1 = S a1,  x2 = S (w1 a2),  z1 = S (w1 r1)
 //   u1 = x1,  u2 = x2 + u1 (b1.a2) + v1 (k1.a2),  y1 = z1 + u1 (b1.r1) + v1 (k1.r1)
 //   S <- S diag(w1 w2) + u1 (w2 b1)^T + v1 (w2 k1)^T + u2 b2^T + v2 k2^T,  y2 = S r2
-// which is also 9 multiplications per element of S instead of 10.  Two producer
+// which is also 9 multiplications per element of S instead of 10.  Four producer
 // warps load the next 16 tokens and form these vectors (the decay costs an
 // exponential and a reciprocal per channel) while the others take the current
-// ones.
+// ones (12 heads of 1024 fp32 tokens, forwards + backwards: 104 + 83 us; with two
+// producer warps 109 + 92, fp16 101 + 80 where four take 103 + 81).
 // What bounds it: the chain of a pair (two dot products, four shuffles, one
-// update: 375 cycles with one row per lane), and with many rows on an SM the
-// reads of each pair's nine vectors from shared memory.  rq_tmix.cu says where it
-// is left for the kernel on the tensor cores.
+// update: 360 cycles with one row per lane, 390 beside the producers), and with
+// many rows on an SM the reads of each pair's nine vectors from shared memory.
+// rq_tmix.cu says where it is left for the kernel on the tensor cores.
 //
 // The backward direction is the same walk with other roles: with G the
 // gradient of the state, for t descending G <- G + dy_t r_t^T, then
@@ -24,6 +25,8 @@
 //   g1 = G (w2 b1) + dy2 (w2 r2 . b1) + g2 (a2.b1) + dy1 (r1.b1)
 //   G <- G diag(w1 w2) + dy2 (w1 w2 r2)^T + g2 (w1 a2)^T + dy1 (w1 r1)^T + g1 a1^T
 // and G is stored behind each chunk of kTmixChunk tokens.
+#include <type_traits>
+
 #include "rq_tmix.cuh"
 
 namespace rq {
@@ -31,8 +34,8 @@ namespace {
 
 constexpr int UNROLL = 4;                    // pairs
 constexpr int CT = kTmixChunk;               // tokens staged at once
-constexpr int NPW = 2;                       // producer warps: a pair of tokens and 8 channels per thread
-static_assert(NPW * 32 == CT / 2 * kHead / 8);
+constexpr int NPW = 4;                       // producer warps: a pair of tokens and 4 channels per thread
+static_assert(NPW * 32 == CT / 2 * kHead / 4);
 // staged vectors of a pair.  Forward: w1 w2 - 1, a1, w1 a2, w1 r1, w2 b1, w2 k1, b2, k2, r2; backward: w1 w2 - 1, b2,
 // w2 b1, w1 w2 r2, w1 a2, w1 r1, a1
 constexpr int nvec(bool rev) { return rev ? 7 : 9; }
@@ -50,27 +53,45 @@ struct Smem {
 };
 
 // The producers' part of a chunk: tokens [t0, t0 + nt) of head h, from global
-// memory into registers (8 channels of two neighbouring tokens per thread) ...
-template <int ROWS>
+// memory into registers (4 channels of two neighbouring tokens per thread) ...
+template <typename T>
+struct Raw4 {
+    std::conditional_t<sizeof(T) == 4, uint4, uint2> u;
+};
+template <typename T>
+__device__ __forceinline__ void cvt4(const Raw4<T>& r, float* f) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(&r.u);
+        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    } else {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&r.u.x));
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&r.u.y));
+        f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
+    }
+}
+template <typename T, int ROWS>
 struct Raw {
-    Raw8 in[2][5];                           // r, d, k, a, b (k forward only)
+    Raw4<T> in[2][5];                        // r, d, k, a, b (k forward only)
     Raw8 row[(CT * ROWS / 8 + NPW * 32 - 1) / (NPW * 32)];
 };
 template <typename T, int ROWS, bool REV>
-__device__ __forceinline__ void load_chunk(const TmixArgs& p, Raw<ROWS>& raw, int64_t t0, int nt, int h, int row0,
+__device__ __forceinline__ void load_chunk(const TmixArgs& p, Raw<T, ROWS>& raw, int64_t t0, int nt, int h, int row0,
                                            int pt) {
     const int64_t head = static_cast<int64_t>(h) * kHead;
-    const int c = (pt & 7) * 8;
+    const int c = (pt & 15) * 4;
+    const auto get = [](const void* from, int64_t at) {
+        return Raw4<T>{__ldg(reinterpret_cast<const decltype(Raw4<T>::u)*>(static_cast<const T*>(from) + at))};
+    };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int t = 2 * (pt >> 3) + i;
+        const int t = 2 * (pt >> 4) + i;
         if (t >= nt) continue;
         const int64_t at = (t0 + t) * p.ld + head + c;
-        raw.in[i][0] = load8(static_cast<const T*>(p.in[0]) + at);
-        raw.in[i][1] = load8(static_cast<const T*>(p.in[1]) + at);
-        if (!REV) raw.in[i][2] = load8(static_cast<const T*>(p.in[2]) + at);
-        raw.in[i][3] = load8(static_cast<const T*>(p.in[4]) + at);
-        raw.in[i][4] = load8(static_cast<const T*>(p.in[5]) + at);
+        raw.in[i][0] = get(p.in[0], at);
+        raw.in[i][1] = get(p.in[1], at);
+        if (!REV) raw.in[i][2] = get(p.in[2], at);
+        raw.in[i][3] = get(p.in[4], at);
+        raw.in[i][4] = get(p.in[5], at);
     }
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(raw.row) / sizeof(Raw8)); ++i) {
@@ -84,28 +105,28 @@ __device__ __forceinline__ void load_chunk(const TmixArgs& p, Raw<ROWS>& raw, in
 // ... and from there, as the vectors of the pairs, into a stage.  A token behind the last of the sequence is one that
 // changes nothing: zeros, and a decay of 1.
 template <typename T, int ROWS, bool REV>
-__device__ __forceinline__ void stage_chunk(Stage<ROWS, REV>& st, const Raw<ROWS>& raw, int nt, int pt) {
-    const int pair = pt >> 3, c = (pt & 7) * 8;
-    if (2 * pair < nt) {                     // whole groups of eight threads
-        float r[2][8], w[2][8], k[2][8], a[2][8], b[2][8];
+__device__ __forceinline__ void stage_chunk(Stage<ROWS, REV>& st, const Raw<T, ROWS>& raw, int nt, int pt) {
+    const int pair = pt >> 4, c = (pt & 15) * 4;
+    if (2 * pair < nt) {                     // whole groups of 16 threads
+        float r[2][4], w[2][4], k[2][4], a[2][4], b[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const bool in = 2 * pair + i < nt;
-            cvt8<T>(raw.in[i][0], r[i]);
-            cvt8<T>(raw.in[i][1], w[i]);
-            cvt8<T>(raw.in[i][3], a[i]);
-            cvt8<T>(raw.in[i][4], b[i]);
-            if (!REV) cvt8<T>(raw.in[i][2], k[i]);
+            cvt4<T>(raw.in[i][0], r[i]);
+            cvt4<T>(raw.in[i][1], w[i]);
+            cvt4<T>(raw.in[i][3], a[i]);
+            cvt4<T>(raw.in[i][4], b[i]);
+            if (!REV) cvt4<T>(raw.in[i][2], k[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 w[i][j] = in ? decay_m1(w[i][j]) : 0.f;
                 if (i == 1 && !in) r[i][j] = a[i][j] = b[i][j] = k[i][j] = 0.f;
             }
         }
-        float f[nvec(REV)][8];
+        float f[nvec(REV)][4];
         float4 dots = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
             // x (1 + m): one rounding
             const float m1 = w[0][j], m2 = w[1][j];
             f[0][j] = fmaf(m1, m2, m1 + m2);
@@ -140,19 +161,17 @@ __device__ __forceinline__ void stage_chunk(Stage<ROWS, REV>& st, const Raw<ROWS
         }
 #pragma unroll
         for (int v = 0; v < nvec(REV); ++v) {
-            float4* to = reinterpret_cast<float4*>(&st.vec[v][pair][c]);
-            to[0] = make_float4(f[v][0], f[v][1], f[v][2], f[v][3]);
-            to[1] = make_float4(f[v][4], f[v][5], f[v][6], f[v][7]);
+            *reinterpret_cast<float4*>(&st.vec[v][pair][c]) = make_float4(f[v][0], f[v][1], f[v][2], f[v][3]);
         }
-        const uint32_t mates = 0xffu << (threadIdx.x & 24);
+        const uint32_t mates = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
+        for (int o = 1; o < 16; o <<= 1) {
             dots.x += __shfl_xor_sync(mates, dots.x, o);
             dots.y += __shfl_xor_sync(mates, dots.y, o);
             dots.z += __shfl_xor_sync(mates, dots.z, o);
             dots.w += __shfl_xor_sync(mates, dots.w, o);
         }
-        if ((pt & 7) == 0) st.dots[pair] = dots;
+        if ((pt & 15) == 0) st.dots[pair] = dots;
     }
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(raw.row) / sizeof(Raw8)); ++i) {
@@ -230,7 +249,7 @@ __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_pairs_kernel(const Tmix
     if (warp >= NCW) {                       // producers
         // a chunk's loads are issued one chunk ahead of its conversion
         const int pt = threadIdx.x - NCW * 32;
-        Raw<ROWS> raw;
+        Raw<T, ROWS> raw;
         const auto load = [&](int c) {
             if (c < nchunk)
                 load_chunk<T, ROWS, REV>(p, raw, lo + static_cast<int64_t>(chunk_of(c)) * CT, tokens_in(chunk_of(c)),
