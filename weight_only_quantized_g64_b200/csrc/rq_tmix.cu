@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(128) tmix_step_kernel(const TmixArgs p) {
 cudaError_t launch_tmix_scan(const TmixArgs& a, bool half, bool reverse, cudaStream_t s) {
     // Up to a head (of all sequences together) for every four SMs, most SMs would be
     // without one of this kernel's CTAs, and its first chunk takes 10 us; pairs of
-    // tokens split a head over four or eight CTAs.  Forwards + backwards in us, pairs /
+    // tokens split a head over eight CTAs.  Forwards + backwards in us, pairs /
     // this kernel: 12 heads of 128 tokens 16 + 13 / 27 + 21, of 1024 101 + 81 / 180 +
     // 150; 32 heads of 512 65 + 49 / 94 + 77; 64 of 512 96 + 78 / 97 + 78, of 1024
     // (forwards) 185 / 173; 128 of 512 188 + 110 / 98 + 79.

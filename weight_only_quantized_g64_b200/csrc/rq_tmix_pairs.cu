@@ -2,7 +2,8 @@
 // of tokens in plain fp32 arithmetic.
 //
 // The rows of the state are spread over lanes and stay in registers for the
-// whole sequence: eight lanes share a row (8 keys each), a lane holds RPL rows.
+// whole sequence: eight lanes share a row (8 keys each), eight CTAs a head (with
+// four, and two rows per lane, 12 heads of 1024 tokens took 123 us for 101).
 // Tokens are taken in pairs, so that one reduction over the eight lanes serves
 // two:
 //   x1 = S a1,  x2 = S (w1 a2),  z1 = S (w1 r1)
@@ -33,6 +34,8 @@ namespace rq {
 namespace {
 
 constexpr int UNROLL = 4;                    // pairs
+constexpr int RPL = 1, NCW = 2;              // rows per lane, row warps of a CTA
+constexpr int ROWS = NCW * 4 * RPL;          // of a CTA: a head is spread over eight
 constexpr int CT = kTmixChunk;               // tokens staged at once
 constexpr int NPW = 4;                       // producer warps: a pair of tokens and 4 channels per thread
 static_assert(NPW * 32 == CT / 2 * kHead / 4);
@@ -40,15 +43,15 @@ static_assert(NPW * 32 == CT / 2 * kHead / 4);
 // w2 b1, w1 w2 r2, w1 a2, w1 r1, a1
 constexpr int nvec(bool rev) { return rev ? 7 : 9; }
 
-template <int ROWS, bool REV>
+template <bool REV>
 struct Stage {
     float vec[nvec(REV)][CT / 2][kHead];
     float row[CT][ROWS];                     // v, or dy
     float4 dots[CT / 2];                     // b1.a2, k1.a2, b1.r1, k1.r1; backward r2.b2, w2 r2.b1, a2.b1, r1.b1
 };
-template <int ROWS, bool REV>
+template <bool REV>
 struct Smem {
-    Stage<ROWS, REV> st[2];
+    Stage<REV> st[2];
     float y[REV ? 1 : 2][REV ? 1 : CT][ROWS];
 };
 
@@ -69,13 +72,13 @@ __device__ __forceinline__ void cvt4(const Raw4<T>& r, float* f) {
         f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
     }
 }
-template <typename T, int ROWS>
+template <typename T>
 struct Raw {
     Raw4<T> in[2][5];                        // r, d, k, a, b (k forward only)
     Raw8 row[(CT * ROWS / 8 + NPW * 32 - 1) / (NPW * 32)];
 };
-template <typename T, int ROWS, bool REV>
-__device__ __forceinline__ void load_chunk(const TmixArgs& p, Raw<T, ROWS>& raw, int64_t t0, int nt, int h, int row0,
+template <typename T, bool REV>
+__device__ __forceinline__ void load_chunk(const TmixArgs& p, Raw<T>& raw, int64_t t0, int nt, int h, int row0,
                                            int pt) {
     const int64_t head = static_cast<int64_t>(h) * kHead;
     const int c = (pt & 15) * 4;
@@ -104,8 +107,8 @@ __device__ __forceinline__ void load_chunk(const TmixArgs& p, Raw<T, ROWS>& raw,
 }
 // ... and from there, as the vectors of the pairs, into a stage.  A token behind the last of the sequence is one that
 // changes nothing: zeros, and a decay of 1.
-template <typename T, int ROWS, bool REV>
-__device__ __forceinline__ void stage_chunk(Stage<ROWS, REV>& st, const Raw<T, ROWS>& raw, int nt, int pt) {
+template <typename T, bool REV>
+__device__ __forceinline__ void stage_chunk(Stage<REV>& st, const Raw<T>& raw, int nt, int pt) {
     const int pair = pt >> 4, c = (pt & 15) * 4;
     if (2 * pair < nt) {                     // whole groups of 16 threads
         float r[2][4], w[2][4], k[2][4], a[2][4], b[2][4];
@@ -217,7 +220,7 @@ __device__ __forceinline__ void sum_lanes(float (&v)[N], float (&o)[N], int lane
     }
 }
 
-template <typename T, int ROWS>
+template <typename T>
 __device__ __forceinline__ void store_y(const TmixArgs& p, const float (*y)[ROWS], int64_t t0, int nt, int h,
                                         int row0, int pt) {
     T* out = static_cast<T*>(p.out[0]);
@@ -228,11 +231,11 @@ __device__ __forceinline__ void store_y(const TmixArgs& p, const float (*y)[ROWS
 }
 
 // One CTA: NCW compute warps of 4 RPL rows each, of one head of one sequence.
-template <typename T, int RPL, int NCW, bool REV>
+template <typename T, bool REV>
 __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_pairs_kernel(const TmixArgs p) {
-    constexpr int ROWS = NCW * 4 * RPL, SPLIT = kHead / ROWS;
+    constexpr int SPLIT = kHead / ROWS;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    Smem<ROWS, REV>& sm = *reinterpret_cast<Smem<ROWS, REV>*>(smem_raw);
+    Smem<REV>& sm = *reinterpret_cast<Smem<REV>*>(smem_raw);
 
     const int part = blockIdx.x % SPLIT;
     const int h = (blockIdx.x / SPLIT) % p.H;
@@ -249,14 +252,14 @@ __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_pairs_kernel(const Tmix
     if (warp >= NCW) {                       // producers
         // a chunk's loads are issued one chunk ahead of its conversion
         const int pt = threadIdx.x - NCW * 32;
-        Raw<T, ROWS> raw;
+        Raw<T> raw;
         const auto load = [&](int c) {
             if (c < nchunk)
-                load_chunk<T, ROWS, REV>(p, raw, lo + static_cast<int64_t>(chunk_of(c)) * CT, tokens_in(chunk_of(c)),
+                load_chunk<T, REV>(p, raw, lo + static_cast<int64_t>(chunk_of(c)) * CT, tokens_in(chunk_of(c)),
                                          h, row0, pt);
         };
         const auto stage = [&](int c) {
-            if (c < nchunk) stage_chunk<T, ROWS, REV>(sm.st[c & 1], raw, tokens_in(chunk_of(c)), pt);
+            if (c < nchunk) stage_chunk<T, REV>(sm.st[c & 1], raw, tokens_in(chunk_of(c)), pt);
         };
         load(0);
         stage(0);
@@ -266,13 +269,13 @@ __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_pairs_kernel(const Tmix
             stage(c + 1);
             load(c + 2);
             if constexpr (!REV) {
-                if (c > 0) store_y<T, ROWS>(p, sm.y[(c - 1) & 1], lo + static_cast<int64_t>(c - 1) * CT, CT, h,
+                if (c > 0) store_y<T>(p, sm.y[(c - 1) & 1], lo + static_cast<int64_t>(c - 1) * CT, CT, h,
                                             row0, pt);
             }
             __syncthreads();
         }
         if constexpr (!REV) {
-            if (nchunk > 0) store_y<T, ROWS>(p, sm.y[(nchunk - 1) & 1], lo + static_cast<int64_t>(nchunk - 1) * CT,
+            if (nchunk > 0) store_y<T>(p, sm.y[(nchunk - 1) & 1], lo + static_cast<int64_t>(nchunk - 1) * CT,
                                              tokens_in(nchunk - 1), h, row0, pt);
         }
         return;
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_pairs_kernel(const Tmix
     for (int c = 0; c < nchunk; ++c) {
         const int ch = chunk_of(c), nt = tokens_in(ch), pairs = (nt + 1) / 2;
         if (ck != nullptr) store_state(ck + ((ckpt_base(lo, seq) + ch) * p.H + h) * kHead * kHead);
-        const Stage<ROWS, REV>& st = sm.st[c & 1];
+        const Stage<REV>& st = sm.st[c & 1];
         // y of a pair is summed over the lanes while the next pair's products are on their way
         float last[2 * RPL] = {};
         const auto write_y = [&](int pair) {             // last[0]: this lane's sum
@@ -411,30 +414,20 @@ __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_pairs_kernel(const Tmix
     if (p.state_out != nullptr && slot >= 0) store_state(p.state_out + head_state);
 }
 
-template <typename T, int RPL, int NCW, bool REV>
-cudaError_t launch_scan(const TmixArgs& a, cudaStream_t s) {
-    constexpr int ROWS = NCW * 4 * RPL;
-    constexpr size_t smem = sizeof(Smem<ROWS, REV>);
-    const cudaError_t e = allow_smem<tmix_pairs_kernel<T, RPL, NCW, REV>>(smem);
-    if (e != cudaSuccess) return e;
-    tmix_pairs_kernel<T, RPL, NCW, REV><<<a.S * a.H * (kHead / ROWS), (NCW + NPW) * 32, smem, s>>>(a);
-    return cudaGetLastError();
-}
-
-// One row per lane, 8 rows and two row warps per CTA, while an SM has at most two
-// such CTAs; else two rows per lane (12 heads of 1024 tokens 101 us and 123, 64 of
-// 512 178 and 96).
 template <typename T, bool REV>
-cudaError_t scan_by_size(const TmixArgs& a, cudaStream_t s) {
-    return static_cast<int64_t>(a.S) * a.H * 8 <= 2 * num_sms() ? launch_scan<T, 1, 2, REV>(a, s)
-                                                                : launch_scan<T, 2, 2, REV>(a, s);
+cudaError_t launch_scan(const TmixArgs& a, cudaStream_t s) {
+    constexpr size_t smem = sizeof(Smem<REV>);
+    const cudaError_t e = allow_smem<tmix_pairs_kernel<T, REV>>(smem);
+    if (e != cudaSuccess) return e;
+    tmix_pairs_kernel<T, REV><<<a.S * a.H * (kHead / ROWS), (NCW + NPW) * 32, smem, s>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_tmix_pairs(const TmixArgs& a, bool half, bool reverse, cudaStream_t s) {
-    if (half) return reverse ? scan_by_size<__half, true>(a, s) : scan_by_size<__half, false>(a, s);
-    return reverse ? scan_by_size<float, true>(a, s) : scan_by_size<float, false>(a, s);
+    if (half) return reverse ? launch_scan<__half, true>(a, s) : launch_scan<__half, false>(a, s);
+    return reverse ? launch_scan<float, true>(a, s) : launch_scan<float, false>(a, s);
 }
 
 }  // namespace rq
