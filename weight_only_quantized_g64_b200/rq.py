@@ -488,12 +488,13 @@ def _heads(call: str, names: str, tensors):
         raise RQError(ERR_RANGE, f"{call}: {names[0]} must be float32 or float16, not {dtype}")
     T, H = shape[0], shape[1]
     ld = stride[0] if T > 1 else H * HEAD
+    rows = (ld, HEAD, 1)
     for n, t in zip(names, tensors):
-        if t.shape != shape or t.dtype is not dtype or t.get_device() != at:
+        if t is not x and (t.shape != shape or t.dtype is not dtype or t.get_device() != at):
             raise RQError(ERR_SHAPE, f"{call}: {n} must be {dtype} {tuple(shape)} on {x.device} like {names[0]}, "
                                      f"not {t.dtype} {tuple(t.shape)} on {t.device}")
         st = t.stride()
-        if st != (ld, HEAD, 1) and t.numel() and (
+        if st != rows and t.numel() and (
                 st[2] != 1 or (H > 1 and st[1] != HEAD) or (T > 1 and st[0] != ld)):
             raise RQError(ERR_SHAPE, f"{call}: {n} must have strides ({ld}, {HEAD}, 1), not {st}")
     return T, H, ld, at
@@ -545,9 +546,11 @@ def tmix_scan(r, d, k, v, a, b, seq_start, state=None, state_out=None, slots=Non
     if state_out is None and slots is None:
         state_out = torch.empty_like(state) if state is not None else \
             torch.empty((S, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
-    _check(lib().rq_tmix_scan(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), T, H, ld, _REAL[r.dtype], _p(seq_start), S,
-                              _p(state), _p(state_out), _p(slots), n, _p(y), _p(ckpt), _p(dev_status),
-                              _stream_of(at)), c)
+    st = lib().rq_tmix_scan(r.data_ptr(), d.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), T, H, ld,
+                            _REAL[r.dtype], seq_start.data_ptr(), S, _p(state), _p(state_out), _p(slots), n,
+                            y.data_ptr(), _p(ckpt), _p(dev_status), _stream_of(at))
+    if st != OK:
+        raise RQError(st, c)
     return y, state_out
 
 
@@ -594,8 +597,11 @@ def tmix_step(r, d, k, v, a, b, state=None, state_out=None, slots=None, y=None, 
     if state_out is None and slots is None:
         state_out = torch.empty_like(state) if state is not None else \
             torch.empty((B, H, HEAD, HEAD), dtype=torch.float32, device=r.device)
-    _check(lib().rq_tmix_step(_p(r), _p(d), _p(k), _p(v), _p(a), _p(b), B, H, ld, _REAL[r.dtype], _p(state),
-                              _p(state_out), _p(slots), n, _p(y), _p(dev_status), _stream_of(at)), c)
+    st = lib().rq_tmix_step(r.data_ptr(), d.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), B, H, ld,
+                            _REAL[r.dtype], _p(state), _p(state_out), _p(slots), n, y.data_ptr(), _p(dev_status),
+                            _stream_of(at))
+    if st != OK:
+        raise RQError(st, c)
     return y, state_out
 
 
