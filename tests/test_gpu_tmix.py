@@ -435,3 +435,29 @@ def test_offsets_past_32_bits(H):
     assert torch.equal(y[T - last:], y1) and torch.equal(end, end1) and torch.equal(start, start1)
     for p, q in zip(grads, grads1):
         assert torch.equal(p[T - last:], q)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("lens", [[33], [48], [64], [65, 0, 129], [400]], ids=str)
+def test_gradients_of_many_heads_by_chunks(lens, dtype):
+    """From the first chunk that a preparing group takes while its last one may still be in use: against fp64, and the
+    same bits every time."""
+    starts = np.cumsum([0] + lens).tolist()
+    T, S, H = starts[-1], len(lens), 40
+    xs = inputs(T, H, dtype, seed=T)
+    g = torch.Generator().manual_seed(T)
+    dstate = (0.1 * torch.randn((S, H, HEAD, HEAD), generator=g)).cuda()
+    dy = torch.randn((T, H, HEAD), generator=g).to(dtype).cuda()
+    seq = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    ckpt = rq.tmix_ckpt(xs[0], S)
+    out, end = rq.tmix_scan(*xs, seq, ckpt=ckpt)
+    got, dstart = rq.tmix_scan_bwd(*xs, seq, ckpt, dy, dstate_out=dstate)
+    ref_y, ref_S, ref_g, ref_G = reference(xs, starts, None, dy, dstate)
+    check(out, ref_y, "y")
+    check(end, ref_S, "state")
+    for n, x, ref in zip("rdkvab", got, ref_g):
+        check(x, ref, "d" + n, times=2.0 if n == "d" else 1.0)
+    check(dstart, ref_G, "dstate")
+    for _ in range(20):
+        again, dagain = rq.tmix_scan_bwd(*xs, seq, ckpt, dy, dstate_out=dstate)
+        assert torch.equal(dstart, dagain) and all(torch.equal(p, q) for p, q in zip(got, again))

@@ -70,6 +70,9 @@ struct alignas(16) Group {
     float x[C][LA], R[C][LA];                // the chunk in preparation: A / B, R
     float y[REV ? C : 1][LB];                // - / A'
     float abt[C][LS], rb[C][LS], t[C][LS];   // M(A B^T) transposed, L(R B^T), T
+    // the warps' own products of the decay.  Memory of their own: they are written before the group first meets in a
+    // chunk, when a slower warp may still read any of the above for the chunk before
+    float parts[4][kHead];
     float ak[REV ? 1 : C][LS], rk[REV ? 1 : C][LS], n[REV ? 1 : C][LS];
 };
 template <typename T, bool REV>
@@ -181,15 +184,13 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
         reinterpret_cast<float4*>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
         reinterpret_cast<float4*>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
     };
-    float (*parts)[kHead] = reinterpret_cast<float (*)[kHead]>(&sm.t[0][0]);     // (t comes later)
-    static_assert(sizeof(sm.t) >= 4 * kHead * sizeof(float));
-    if (lane >= 24) put8(&parts[warp][k0], w);
+    if (lane >= 24) put8(&sm.parts[warp][k0], w);
     group_sync(group);
     float before[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) before[j] = 1.f;
     for (int i = 0; i < warp; ++i) {
-        const float4 x = *reinterpret_cast<const float4*>(&parts[i][k0]), y = *reinterpret_cast<const float4*>(&parts[i][k0 + 4]);
+        const float4 x = *reinterpret_cast<const float4*>(&sm.parts[i][k0]), y = *reinterpret_cast<const float4*>(&sm.parts[i][k0 + 4]);
         before[0] *= x.x; before[1] *= x.y; before[2] *= x.z; before[3] *= x.w;
         before[4] *= y.x; before[5] *= y.y; before[6] *= y.z; before[7] *= y.w;
     }
