@@ -461,3 +461,74 @@ def test_gradients_of_many_heads_by_chunks(lens, dtype):
     for _ in range(20):
         again, dagain = rq.tmix_scan_bwd(*xs, seq, ckpt, dy, dstate_out=dstate)
         assert torch.equal(dstart, dagain) and all(torch.equal(p, q) for p, q in zip(got, again))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("H", [2, 40])
+def test_slow_decays(H, dtype):
+    """Decays near 1, the same in every token of a long sequence: what a rounding of each would lose adds up.
+
+    The keys 32 .. 63 have a = b = 0, so every element of their states is w S + v k in each token; d runs over them
+    from -12 to -7, v k is small against the first state, and the outputs read these keys alone.  With u = 2^-24 and M
+    the largest magnitude of a state, a chunk of 16 tokens rounds an element twice (the sum, the decay) and a pair or
+    a single token at most three times for two: 3 u M T / 2 if every rounding has one sign in the worst form, 2 u M T /
+    16 in the chunks.  log w, off by at most (|d| + 6) u of itself, adds T |log w| w^T (|d| + 6) u <= 18 u.  The
+    products v k are kept to 2^-21: T of them, together at most 2^-21 T max|v| max|k| (backwards dy, r).  An output is a
+    sum of 32 products, each kept to 2^-21 as well.
+    """
+    T, u = 4096, 2.0 ** -24
+    g = torch.Generator().manual_seed(H)
+    r, d, k, v, a, b = inputs(T, H, torch.float32, seed=H)
+    v, d = 0.01 * v, d.clone()
+    d[:, :, 32:] = torch.linspace(-12, -7, 32)
+    for x in (a, b):
+        x[:, :, 32:] = 0
+    r[:, :, :32] = 0
+    xs = [x.to(dtype) for x in (r, d, k, v, a, b)]
+    dy = (0.01 * torch.randn((T, H, HEAD), generator=g)).to(dtype).cuda()
+    state, dstate = ((10 * torch.randn((1, H, HEAD, HEAD), generator=g)).cuda() for _ in range(2))
+    seq = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    ckpt = rq.tmix_ckpt(xs[0], 1)
+    y, end = rq.tmix_scan(*xs, seq, state=state, ckpt=ckpt)
+    _, start = rq.tmix_scan_bwd(*xs, seq, ckpt, dy, dstate_out=dstate)
+    n = 2                                    # heads that are compared
+    R, D, K, V, dY = (x[:, :n].double().cpu().numpy() for x in (*xs[:4], dy))
+    w = np.exp(-DECAY / (1 + np.exp(-D)))[:, :, None, 32:]
+    S, G = (x[0, :n, :, 32:].double().cpu().numpy() for x in (state, dstate))
+    M, N = np.abs(S).max(), np.abs(G).max()
+    rounds = 2 * T / 16 if H == 40 else 1.5 * T
+    lim = (rounds + 18) * u * M + 2.0 ** -21 * T * np.abs(V).max() * np.abs(K).max()
+    out = y[:, :n].double().cpu().numpy()
+    for t in range(T):
+        S = S * w[t] + V[t][:, :, None] * K[t][:, None, 32:]
+        ref, r1 = np.einsum("hij,hj->hi", S, R[t][:, 32:]), np.abs(R[t]).sum(1, keepdims=True)
+        half = np.abs(ref) * 2.0 ** -11 + 2.0 ** -25 if dtype == torch.float16 else 0.0
+        assert np.all(np.abs(out[t] - ref) <= r1 * (lim + 2.0 ** -20 * M) + half), t
+    for t in reversed(range(T)):
+        G = (G + dY[t][:, :, None] * R[t][:, None, 32:]) * w[t]
+    for got, ref, top, f in ((end, S, M, np.abs(V).max() * np.abs(K).max()), (start, G, N, np.abs(dY).max() * np.abs(R).max())):
+        e = np.abs(got[0, :n, :, 32:].double().cpu().numpy() - ref).max()
+        assert e <= (rounds + 18) * u * top + 2.0 ** -21 * T * f, (e, top)
+
+
+@pytest.mark.parametrize("H", [2, 40])
+def test_strong_decays(H):
+    """States that do nothing but decay, through products of down to 6e-5 in 16 tokens, element by element: with
+    u = 2^-24 a token multiplies by w, off by 0.61 * 2^-21 (the sigmoid's error) and rounded, and rounds the product: at
+    most 7 u.  The chunks of 16 add up log2 w instead, at most 14 and so with roundings of 8 u in four sums, and take 2^x,
+    good to 4 u: 5 u a token and 40 u a chunk."""
+    T = 75
+    xs = inputs(T, H, torch.float32, seed=H)
+    for i in (2, 3, 4, 5):
+        xs[i].zero_()
+    xs[1][:] = torch.linspace(-4, 20, HEAD)
+    g = torch.Generator().manual_seed(H)
+    state, dstate = (torch.randn((1, H, HEAD, HEAD), generator=g).cuda() for _ in range(2))
+    seq = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    ckpt = rq.tmix_ckpt(xs[0], 1)
+    _, end = rq.tmix_scan(*xs, seq, state=state, ckpt=ckpt)
+    _, start = rq.tmix_scan_bwd(*xs, seq, ckpt, torch.zeros_like(xs[0]), dstate_out=dstate)
+    w = torch.exp(-DECAY * T * torch.sigmoid(xs[1][0, 0].double()))
+    for got, first in ((end, state), (start, dstate)):
+        ref = first.double() * w
+        assert torch.all((got.double() - ref).abs() <= 8 * T * 2.0 ** -24 * ref.abs())

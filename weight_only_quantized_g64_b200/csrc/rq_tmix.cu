@@ -60,7 +60,10 @@ struct alignas(16) Chunk {
     float r[REV ? 1 : C][LA];
     float b[C][LB], k[C][LB];
     float m[REV ? 1 : C][LS];
-    float last[kHead];                       // W of the last token
+    // W of the last token as x + y, applied as S x + S y: (W - 1, 1) above 1/2, where S W = S + S (W - 1) keeps W's
+    // distance from 1 (W itself, rounded to 24 bits, would carry the same error into the state in every chunk), and
+    // (W, 0) below, where W - 1 would lose W's own bits
+    float2 last[kHead];
     T v[C][kHead + 8];
     int bad;                                 // a value of the chunk is not finite
 };
@@ -70,8 +73,8 @@ struct alignas(16) Group {
     float x[C][LA], R[C][LA];                // the chunk in preparation: A / B, R
     float y[REV ? C : 1][LB];                // - / A'
     float abt[C][LS], rb[C][LS], t[C][LS];   // M(A B^T) transposed, L(R B^T), T
-    // the warps' own products of the decay.  Memory of their own: they are written before the group first meets in a
-    // chunk, when a slower warp may still read any of the above for the chunk before
+    // log2 W of the warps' own tokens.  Memory of its own: it is written before the group first meets in a chunk, when
+    // a slower warp may still read any of the above for the chunk before
     float parts[4][kHead];
     float ak[REV ? 1 : C][LS], rk[REV ? 1 : C][LS], n[REV ? 1 : C][LS];
 };
@@ -152,7 +155,7 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
         for (int j = 0; j < 8; ++j) {
             sum += (fabsf(r[j]) + fabsf(a[j])) + (fabsf(b[j]) + (REV ? 0.f : fabsf(k[j])));
             bad |= w[j] != w[j];
-            w[j] = in ? decay_m1(w[j]) : 0.f;
+            w[j] = in ? log2_decay(w[j]) : 0.f;
         }
         bad |= !(sum < 1e30f);               // (and none so large that its product with 1 / W is not finite)
         next();                              // the inputs of the chunk after this one, into raw
@@ -171,46 +174,44 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
             return;
         }
     }
-    // W: products over the tokens, in the warp and then of the warps before
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        w[j] += 1.f;
-        float o = __shfl_up_sync(0xffffffffu, w[j], 8);
-        w[j] *= lane >= 8 ? o : 1.f;
-        o = __shfl_up_sync(0xffffffffu, w[j], 16);
-        w[j] *= lane >= 16 ? o : 1.f;
-    }
     const auto put8 = [](float* to, const float* f) {
         reinterpret_cast<float4*>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
         reinterpret_cast<float4*>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
     };
+    // log2 W: sums over the tokens, in the warp and then of the warps before
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float o = __shfl_up_sync(0xffffffffu, w[j], 8);
+        w[j] += lane >= 8 ? o : 0.f;
+        o = __shfl_up_sync(0xffffffffu, w[j], 16);
+        w[j] += lane >= 16 ? o : 0.f;
+    }
     if (lane >= 24) put8(&sm.parts[warp][k0], w);
     group_sync(group);
     float before[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) before[j] = 1.f;
+    for (int j = 0; j < 8; ++j) before[j] = 0.f;
     for (int i = 0; i < warp; ++i) {
         const float4 x = *reinterpret_cast<const float4*>(&sm.parts[i][k0]), y = *reinterpret_cast<const float4*>(&sm.parts[i][k0 + 4]);
-        before[0] *= x.x; before[1] *= x.y; before[2] *= x.z; before[3] *= x.w;
-        before[4] *= y.x; before[5] *= y.y; before[6] *= y.z; before[7] *= y.w;
+        before[0] += x.x; before[1] += x.y; before[2] += x.z; before[3] += x.w;
+        before[4] += y.x; before[5] += y.y; before[6] += y.z; before[7] += y.w;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float up = __shfl_up_sync(0xffffffffu, w[j], 8);
-        const float prev = before[j] * (lane >= 8 ? up : 1.f);
-        w[j] *= before[j];
-        float back;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(back) : "f"(w[j]));
-        r[j] *= w[j];
+        const float prev = exp2_approx(before[j] + (lane >= 8 ? up : 0.f));
+        w[j] += before[j];
+        const float W = exp2_approx(w[j]), back = exp2_approx(-w[j]);
+        r[j] *= W;
         a[j] *= prev;
         b[j] *= back;
         if (!REV) k[j] *= back;
+        if (token == C - 1) ch.last[k0 + j] = w[j] > -1.f ? make_float2(expm1_near(w[j] * kLn2), 1.f) : make_float2(W, 0.f);
     }
     put8(&sm.R[token][k0], r);
     put8(REV ? &ch.b[token][k0] : &sm.x[token][k0], a);
     put8(REV ? &sm.x[token][k0] : &ch.b[token][k0], b);
     if (!REV) put8(&ch.k[token][k0], k);
-    if (token == C - 1) put8(&ch.last[k0], w);
     group_sync(group);
 
     // the 16 x 16 products, one per warp
@@ -408,11 +409,11 @@ __device__ __forceinline__ void forward_chunk(State& S, const Chunk<T, false>& c
     }
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-        const float2 w = *reinterpret_cast<const float2*>(&ch.last[8 * n + 2 * q]);
-        S[n][0] *= w.x;
-        S[n][1] *= w.y;
-        S[n][2] *= w.x;
-        S[n][3] *= w.y;
+        const float4 w = *reinterpret_cast<const float4*>(&ch.last[8 * n + 2 * q]);
+        S[n][0] = fmaf(S[n][0], w.x, S[n][0] * w.y);
+        S[n][1] = fmaf(S[n][1], w.z, S[n][1] * w.w);
+        S[n][2] = fmaf(S[n][2], w.x, S[n][2] * w.y);
+        S[n][3] = fmaf(S[n][3], w.z, S[n][3] * w.w);
     }
     if (__any_sync(0xffffffffu, min(from[0], from[1]) < C)) {
 #pragma unroll
@@ -479,11 +480,11 @@ __device__ __forceinline__ void backward_chunk(State& G, const Chunk<T, true>& c
     const int g = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-        const float2 w = *reinterpret_cast<const float2*>(&ch.last[8 * n + 2 * q]);
-        G[n][0] *= w.x;
-        G[n][1] *= w.y;
-        G[n][2] *= w.x;
-        G[n][3] *= w.y;
+        const float4 w = *reinterpret_cast<const float4*>(&ch.last[8 * n + 2 * q]);
+        G[n][0] = fmaf(G[n][0], w.x, G[n][0] * w.y);
+        G[n][1] = fmaf(G[n][1], w.z, G[n][1] * w.w);
+        G[n][2] = fmaf(G[n][2], w.x, G[n][2] * w.y);
+        G[n][3] = fmaf(G[n][3], w.z, G[n][3] * w.w);
     }
     Sums<2> X;
     X.clear();

@@ -21,6 +21,7 @@ namespace rq {
 constexpr int kHead = 64;                    // channels of a head
 constexpr int kTmixChunk = 16;               // tokens between two stored states (training)
 constexpr float kDecay = 0.60653065971263342f;   // e^{-1/2}
+constexpr float kLn2 = 0.69314718055994531f;
 
 struct TmixArgs {
     const void* in[6];                       // r, d, k, v, a, b: [T, H, 64], rows ld elements apart
@@ -99,19 +100,20 @@ __device__ __forceinline__ T from_f32(float v) {
 // sigmoid(d), relative error at most (|d| + 6) 2^-24 below 0 and 2^-21 above (the
 // hardware's 2^x and 1/x are good to 2^-22 and 2^-23, d log2(e) is rounded once):
 // it scales log w, which is small where that grows.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+    return e;
+}
 __device__ __forceinline__ float decay_gate(float d) {
-    float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    float s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + exp2_approx(d * -1.4426950408889634f)));
     return s;
 }
-// w - 1: the update w S = S + (w - 1) S then rounds S once, and a decay near 1
-// keeps its distance from 1 over thousands of steps (w itself, rounded to 24
-// bits, would be off by up to 2^-25 in every step, in the same direction).
-// e^x - 1 by its series x (1 + x/2! + x^2/3! + ...): -0.61 <= x <= 0, so nine
-// terms leave less than 0.61^9 / 10! < 2^-27 of it.
-__device__ __forceinline__ float decay_m1(float d) {
-    const float x = -kDecay * decay_gate(d);
+__device__ __forceinline__ float log2_decay(float d) { return -kDecay / kLn2 * decay_gate(d); }
+// e^x - 1 for -ln 2 <= x <= 0 by its series x (1 + x/2! + x^2/3! + ...): nine terms
+// leave less than 0.7^9 / 10! < 2^-26 of it.
+__device__ __forceinline__ float expm1_near(float x) {
     float p = 1.f / 362880.f;
     p = fmaf(p, x, 1.f / 40320.f);
     p = fmaf(p, x, 1.f / 5040.f);
@@ -123,6 +125,10 @@ __device__ __forceinline__ float decay_m1(float d) {
     p = fmaf(p, x, 1.f);
     return x * p;
 }
+// w - 1: the update w S = S + (w - 1) S then rounds S once, and a decay near 1
+// keeps its distance from 1 over thousands of steps (w itself, rounded to 24
+// bits, would be off by up to 2^-25 in every step, in the same direction).
+__device__ __forceinline__ float decay_m1(float d) { return expm1_near(-kDecay * decay_gate(d)); }
 
 // --------------------------------------------------------------- sequences --
 // Tokens [lo, hi) of sequence i; false (and a status) for offsets that are
