@@ -532,3 +532,31 @@ def test_strong_decays(H):
     for got, first in ((end, state), (start, dstate)):
         ref = first.double() * w
         assert torch.all((got.double() - ref).abs() <= 8 * T * 2.0 ** -24 * ref.abs())
+
+
+def test_gradient_of_strong_and_weak_decays():
+    """dd = dlogw * -c s (1 - s) where either factor is small, element by element: sequences of one token with k = v =
+    dy = 0, so that dlogw_j = w_j sum_i G_ij S_ij, here of positive terms.
+
+    With u = 2^-24: the sum of 64 products in fp32 is off by at most 66 u of itself, w by 2 u; e^-|d| by 2 |d| u + 4 u (its
+    argument rounded once, beside log2(e); 2^x good to 2^-22), 1 / (1 + e) by that and 3 u; their products add 3 u.
+    Together (66 + 2 + 6 |d| + 24) u."""
+    T, H = 256, 1
+    xs = inputs(T, H, torch.float32, seed=21)
+    for i in (2, 3):
+        xs[i].zero_()
+    xs[1][:] = torch.linspace(-30, 30, T * HEAD).view(T, H, HEAD)
+    g = torch.Generator().manual_seed(21)
+    state, dstate = ((0.1 + torch.rand((T, H, HEAD, HEAD), generator=g)).cuda() for _ in range(2))
+    xs[4].zero_(), xs[5].zero_()
+    seq = torch.arange(T + 1, dtype=torch.int32, device="cuda")
+    ckpt = rq.tmix_ckpt(xs[0], T)
+    rq.tmix_scan(*xs, seq, state=state, ckpt=ckpt)
+    grads, _ = rq.tmix_scan_bwd(*xs, seq, ckpt, torch.zeros_like(xs[0]), dstate_out=dstate)
+    d = xs[1].double().cpu().numpy()
+    s, c = 1 / (1 + np.exp(-d)), 1 / (1 + np.exp(d))
+    sums = (state.double() * dstate.double()).sum(2).cpu().numpy()
+    ref = sums * np.exp(-DECAY * s) * -DECAY * s * c
+    off = np.abs(grads[1].double().cpu().numpy() / ref - 1)
+    lim = (92 + 6 * np.abs(d)) * 2.0 ** -24
+    assert np.all(off <= lim), f"worst {(off / lim).max():.2f} of the bound at d = {d.flat[(off / lim).argmax()]}"

@@ -99,16 +99,25 @@ __device__ __forceinline__ T from_f32(float v) {
 // ------------------------------------------------------------------- decay --
 // sigmoid(d), relative error at most (|d| + 6) 2^-24 below 0 and 2^-21 above (the
 // hardware's 2^x and 1/x are good to 2^-22 and 2^-23, d log2(e) is rounded once):
-// it scales log w, which is small where that grows.
+// it scales log w, which is small where that grows.  Below -87.3, where it would be
+// under 2^-126, it is 0.
 __device__ __forceinline__ float exp2_approx(float x) {
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
     return e;
 }
-__device__ __forceinline__ float decay_gate(float d) {
-    float s;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + exp2_approx(d * -1.4426950408889634f)));
-    return s;
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float exp_minus(float d) { return exp2_approx(d * -1.4426950408889634f); }
+__device__ __forceinline__ float decay_gate(float d) { return rcp_approx(1.f + exp_minus(d)); }
+// Its derivative, s (1 - s).  From 0 on 1 - s is e^-d s, as the difference would lose
+// its bits (9e-3 of it at d = 12, all from 17 on); below, e^-d may be infinite.
+__device__ __forceinline__ float decay_gate_slope(float d) {
+    const float e = exp_minus(d), s = rcp_approx(1.f + e);
+    return s * (d >= 0.f ? e * s : 1.f - s);
 }
 __device__ __forceinline__ float log2_decay(float d) { return -kDecay / kLn2 * decay_gate(d); }
 // e^x - 1 for -ln 2 <= x <= 0 by its series x (1 + x/2! + x^2/3! + ...): nine terms

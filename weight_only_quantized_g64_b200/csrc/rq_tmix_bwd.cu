@@ -334,10 +334,7 @@ __global__ void __launch_bounds__(THREADS, 2) tmix_chunk_bwd_kernel(const TmixAr
     __syncthreads();
     if (in) {
         const float4 g = ld4(&dl[et][ec]);
-        const auto dd = [](float dlogw, float d) {
-            const float s = decay_gate(d);
-            return dlogw * (-kDecay * s * (1.f - s));
-        };
+        const auto dd = [](float dlogw, float d) { return dlogw * (-kDecay * decay_gate_slope(d)); };
         store4(static_cast<T*>(p.out[1]) + out_at, make_float4(dd(g.x, xd.x), dd(g.y, xd.y), dd(g.z, xd.z), dd(g.w, xd.w)));
     }
 }
