@@ -380,7 +380,8 @@ rq_status rq_lora_add(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A
  * sqrt(mean square + eps)), over the whole row or, for post, over post_group
  * channels (0 or D: the row; else 8, 16, .. 256, dividing D), then * weight + bias
  * (fp32 [D] each, or NULL; not used without a norm).  gate_act: RQ_GATE_IDENTITY, RQ_GATE_SIGMOID,
- * RQ_GATE_SILU.  alpha: fp32 [D].  All arithmetic is fp32; Norm_pre reads h'
+ * RQ_GATE_SILU (a sigmoid under 2^-126, of gates below -87.3, counts as 0).
+ * alpha: fp32 [D].  All arithmetic is fp32; Norm_pre reads h'
  * before it is rounded.  D % 64 == 0, 64 <= D <= 16384, M >= 1, strides >= D
  * and multiples of 8, else RQ_ERR_SHAPE; a bad dtype, norm, act or a negative
  * eps: RQ_ERR_RANGE; pointers 16-byte aligned.  Asynchronous on `stream`.

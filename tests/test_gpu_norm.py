@@ -197,3 +197,22 @@ def test_offsets_past_32_bits():
     h1, x1 = rq.norm_residual(y, post="layer", h=h, pre="rms")
     h2, x2 = rq.norm_residual(y[M - last:].contiguous(), post="layer", h=h[M - last:], pre="rms")
     assert torch.equal(h1[M - last:], h2) and torch.equal(x1[M - last:], x2)
+
+
+@pytest.mark.parametrize("D", [512, 8192])
+def test_silu_of_large_and_very_negative_gates(D):
+    """u * gate alone would overflow; the sigmoid by itself is 0 from about -87 on.
+
+    silu is off by at most (2 |g| + 16) u of itself above -87, and below 2^-126 |g| there."""
+    M = 3
+    y = torch.full((M, D), 1e37, device="cuda")
+    y[1] = -3e30
+    gate = torch.linspace(-120, -60, M * D).view(M, D).cuda()
+    gate[2, ::2] = 20.0
+    y[2] = 1e25
+    h, _ = rq.norm_residual(y, gate=gate, gate_act="silu", h=torch.zeros_like(y))
+    g, v = gate.double().cpu().numpy(), y.double().cpu().numpy()
+    ref = v * g / (1 + np.exp(-g))
+    lim = np.where(g > -87, (2 * np.abs(g) + 16) * U * np.abs(ref), np.abs(v * g) * 2.0 ** -126)
+    d = np.abs(h.double().cpu().numpy() - ref)
+    assert np.all(d <= lim), f"worst at gate {g.flat[np.nanargmax(d / lim)]}"

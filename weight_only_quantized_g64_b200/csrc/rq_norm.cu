@@ -233,7 +233,8 @@ __device__ __forceinline__ void normed(Piece (&u)[R][V], int pieces, const NormA
 }
 
 // Relative error at most (|x| + 6) 2^-24 below 0, and 2^-21 above: the hardware's
-// 2^x and 1/x are good to 2^-22 and 2^-23, and x log2(e) is rounded once.
+// 2^x and 1/x are good to 2^-22 and 2^-23, and x log2(e) is rounded once.  Below
+// -87.3, where it would be under 2^-126, it is 0.
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t x) {
     float2 t = unpack2(mul2(x, both(-1.4426950408889634f)));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.x));
@@ -255,12 +256,15 @@ __device__ __forceinline__ void combine(Piece* (&u)[R], const NormArgs& p, int c
     if (p.gate != nullptr) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const Piece g = take(r, p.gate, p.ld_gate);
-            if (p.gate_act != RQ_GATE_SIGMOID) times(*u[r], g);
-            if (p.gate_act != RQ_GATE_IDENTITY) {
+            Piece g = take(r, p.gate, p.ld_gate);
+            if (p.gate_act != RQ_GATE_IDENTITY) {        // act(gate) first: u * gate alone might not be finite
 #pragma unroll
-                for (int j = 0; j < 4; ++j) u[r]->v[j] = mul2(u[r]->v[j], sigmoid2(g.v[j]));
+                for (int j = 0; j < 4; ++j) {
+                    const uint64_t s = sigmoid2(g.v[j]);
+                    g.v[j] = p.gate_act == RQ_GATE_SIGMOID ? s : mul2(g.v[j], s);
+                }
             }
+            times(*u[r], g);
         }
     }
     if (p.alpha != nullptr) {
