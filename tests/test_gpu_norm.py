@@ -216,3 +216,15 @@ def test_silu_of_large_and_very_negative_gates(D):
     lim = np.where(g > -87, (2 * np.abs(g) + 16) * U * np.abs(ref), np.abs(v * g) * 2.0 ** -126)
     d = np.abs(h.double().cpu().numpy() - ref)
     assert np.all(d <= lim), f"worst at gate {g.flat[np.nanargmax(d / lim)]}"
+
+
+@pytest.mark.parametrize("first", [dict(post="rms"), dict(x=None), dict(eps_pre=1e-5), {}], ids=str)
+def test_stream_with_keywords_in_any_order(first, monkeypatch):
+    t = tensors(4, 128, torch.float32, seed=1)
+    side = torch.cuda.Stream()
+    seen, real = [], rq._stream_of
+    monkeypatch.setattr(rq, "_stream_of", lambda at: seen.append(real(at)) or seen[-1])
+    torch.cuda.synchronize()
+    rq.norm_residual(**first, y=t["y"], stream=side)
+    side.synchronize()
+    assert seen == [side.cuda_stream]

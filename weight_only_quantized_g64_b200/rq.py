@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 import re
 
@@ -344,11 +345,13 @@ _REAL = {torch.float32: OUT_F32, torch.float16: OUT_F16}
 
 
 def _placed(fn):
-    """The call runs, and allocates, on its first tensor's device and on the
-    given stream (default: that device's current one)."""
+    """The call runs, and allocates, on the device of its first parameter's
+    tensor and on the given stream (default: that device's current one)."""
+    name = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        first = args[0] if args else next(iter(kw.values()), None)
+        first = args[0] if args else kw.get(name)
         at = first.get_device() if isinstance(first, torch.Tensor) else -1
         if at < 0 or (stream is None and at == _this_device()):
             return fn(*args, **kw)
