@@ -11,6 +11,8 @@ of u, gate (e^-x within 2 u, the division 1 u) and residual on the magnitudes
 that enter, carry e through Norm_pre with its own e and 1 / s, and add half a
 step of fp16 (2^-11 of the value, 2^-25 for subnormals) where an output is fp16.
 """
+import types
+
 import numpy as np
 import pytest
 import torch
@@ -228,3 +230,10 @@ def test_stream_with_keywords_in_any_order(first, monkeypatch):
     rq.norm_residual(**first, y=t["y"], stream=side)
     side.synchronize()
     assert seen == [side.cuda_stream]
+
+
+def test_stream_of_another_device_is_refused():
+    t = tensors(4, 128, torch.float32, seed=1)
+    with pytest.raises(rq.RQError) as e:
+        rq.norm_residual(t["y"], stream=types.SimpleNamespace(device_index=t["y"].get_device() + 1))
+    assert e.value.status == rq.ERR_SHAPE

@@ -355,6 +355,7 @@ def _placed(fn):
         at = first.get_device() if isinstance(first, torch.Tensor) else -1
         if at < 0 or (stream is None and at == _this_device()):
             return fn(*args, **kw)
+        _need(stream is None or stream.device_index == at, f"{fn.__name__}: the stream is not of {first.device}")
         with torch.cuda.device(at), torch.cuda.stream(stream):
             return fn(*args, **kw)
     return call
