@@ -339,8 +339,9 @@ def rkv_fused(x: torch.Tensor, wr, wk, wv, N: int, bits: int, ys=None, stream=No
 HEAD = 64
 
 
-_this_device = torch._C._cuda_getDevice
-_stream_of = torch._C._cuda_getCurrentRawStream      # of a device: the stream's handle alone
+# torch's own short forms of the public calls, where it has them (a torch without CUDA can still import this module)
+_this_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", lambda at: torch.cuda.current_stream(at).cuda_stream)
 _REAL = {torch.float32: OUT_F32, torch.float16: OUT_F16}
 
 
