@@ -634,7 +634,7 @@ cudaError_t launch_scan(const TmixArgs& a, cudaStream_t s) {
 // requests of 64 heads 12.4 us, 5.6 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(128) tmix_step_kernel(const TmixArgs p) {
-    __shared__ float wm1[kHead];
+    __shared__ __align__(16) float wm1[kHead];       // read as float4
     const int h = blockIdx.x % p.H, b = blockIdx.x / p.H;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3;
     const int row = warp * 16 + (lane >> 2);         // and row + 8
