@@ -237,3 +237,18 @@ def test_stream_of_another_device_is_refused():
     with pytest.raises(rq.RQError) as e:
         rq.norm_residual(t["y"], stream=types.SimpleNamespace(device_index=t["y"].get_device() + 1))
     assert e.value.status == rq.ERR_SHAPE
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("M,D", [(2369, 512), (297, 4096), (149, 8192)])
+def test_many_rows_strided_and_in_place(M, D, dtype):
+    t = tensors(M, D, dtype, seed=3)
+    kw = dict(post="rms", pre="layer", gate_act="sigmoid")
+    h1, x1 = rq.norm_residual(**t, **kw)
+    wide = torch.full((M, 3 * D + 40), float("nan"), dtype=dtype, device="cuda")
+    for i, n in enumerate(("y", "add", "gate")):
+        wide[:, 8 + i * D:8 + (i + 1) * D] = t[n]
+        t[n] = wide[:, 8 + i * D:8 + (i + 1) * D]
+    mine = t["h"].clone()
+    h2, x2 = rq.norm_residual(**{**t, "h": mine}, h_out=mine, **kw)
+    assert h2 is mine and torch.equal(h1, mine) and torch.equal(x1, x2)

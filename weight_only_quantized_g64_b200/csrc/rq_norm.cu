@@ -383,7 +383,11 @@ __global__ void __launch_bounds__(512) norm_row_kernel(const NormArgs p) {
         if (i >= pieces) break;
         const int c = (threadIdx.x + i * threads) * 8;
         Piece* rows[1] = {&u[0][i]};
-        combine<1>(rows, p, c, [&](int, const void* base, int64_t ld) { return load<T>(base, row * ld + c); });
+        // (not as read-only data: h may be h_out)
+        combine<1>(rows, p, c, [&](int, const void* base, int64_t ld) {
+            const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + row * ld + c);
+            return expand<T>(from[0], sizeof(T) == 4 ? from[1] : make_uint4(0u, 0u, 0u, 0u));
+        });
         if (p.h_out != nullptr) store<T>(p.h_out, row * p.D + c, u[0][i]);
     }
     if (p.x == nullptr) return;
