@@ -239,6 +239,23 @@ def test_stream_of_another_device_is_refused():
     assert e.value.status == rq.ERR_SHAPE
 
 
+MANY = [(18945, 64), (3789, 320), (2369, 512), (475, 2560), (297, 4096)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("M,D", MANY)
+def test_many_rows(M, D, dtype):
+    """Enough rows to be taken two at a time, the last one by itself; four fp32 tensors of 4096 one at a time all the
+    same."""
+    t = tensors(M, D, dtype, seed=D)
+    run(t, post="layer", post_group=64, pre="rms", gate_act="silu")
+    run(t, post="rms", post_group=8, pre="layer", gate_act="identity")
+    run(t, post="layer", pre="layer", gate_act="sigmoid")
+    run(dict(y=t["y"], h=t["h"], gate=t["gate"]), post="rms", pre="rms", gate_act="silu")
+    run(dict(y=t["y"], h=t["h"]), pre="layer")
+    run(dict(y=t["y"], add=t["add"], post_weight=t["post_weight"]), post="layer", post_group=32)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
 @pytest.mark.parametrize("M,D", [(2369, 512), (297, 4096), (149, 8192)])
 def test_many_rows_strided_and_in_place(M, D, dtype):
@@ -252,3 +269,15 @@ def test_many_rows_strided_and_in_place(M, D, dtype):
     mine = t["h"].clone()
     h2, x2 = rq.norm_residual(**{**t, "h": mine}, h_out=mine, **kw)
     assert h2 is mine and torch.equal(h1, mine) and torch.equal(x1, x2)
+
+
+def test_many_rows_non_finite_stays_in_its_row():
+    M, D = 2369, 512
+    t = tensors(M, D, torch.float32, seed=5)
+    clean_h, clean_x = rq.norm_residual(**t, post="layer", pre="layer")
+    t["y"][7, 5] = float("inf")
+    t["y"][M - 1, 9] = float("nan")
+    h, x = rq.norm_residual(**t, post="layer", pre="layer")
+    rest = [i for i in range(M) if i not in (7, M - 1)]
+    for got, clean in ((h, clean_h), (x, clean_x)):
+        assert torch.isnan(got[[7, M - 1]]).all() and torch.equal(got[rest], clean[rest])
