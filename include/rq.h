@@ -339,7 +339,8 @@ rq_status rq_gemm_wq(const uint16_t *x, int64_t M, int64_t K, const void *codes,
  * caller-zeroed device int) to RQ_ERR_RANGE.  Sums are fp32 (the products of
  * fp16 values exact, t kept to 22 bits or, where it is small, to 2^-38 of the
  * token's largest); out is rounded once.  A value that is not finite reaches
- * its own token, or (in B) its own column, and no other.
+ * its own token, or (in B) its own column of its adapter's tokens, and no other;
+ * what it reaches is not finite, but may be NaN where the formula gives an infinity.
  *
  * x: fp16 [M, K].  A: fp16 [L, R, K].  B: fp16 [L, N, R].  ids: int32 [M].
  * ranks: int32 [L] or NULL (all R); values above R count as R, below 0 as 0;
@@ -409,7 +410,10 @@ rq_status rq_norm_residual(const void *y, int64_t ld_y, int64_t M, int64_t D, in
  *   S_t = S_{t-1} diag(w_t) + (S_{t-1} a_t) b_t^T + v_t k_t^T
  *   y_t = S_t r_t
  * (In the model a = -kappa, b = kappa * gate with a normalised key kappa; here
- * a and b are free.)  All arithmetic is fp32; y is rounded once.
+ * a and b are free.)  States and sums are fp32, y is rounded once.  Where 16
+ * tokens are taken at once (sequences of many heads; the gradients always) the
+ * factors of the products, the states among them, enter with 22 of their 24 bits
+ * (fp16 values exactly); everything else is fp32 arithmetic.
  *
  * r, d, k, v, a, b: [T, H, 64] device, 16-byte aligned, of one type dtype
  * (RQ_OUT_F32 or RQ_OUT_F16, else RQ_ERR_RANGE), tokens ld elements apart
@@ -445,7 +449,8 @@ rq_status rq_norm_residual(const void *y, int64_t ld_y, int64_t M, int64_t D, in
  * db and dstate_in (gradient of the initial states, NULL: dropped).  Same
  * inputs as the forward call, with its ckpt.  work: rq_tmix_ckpt_bytes bytes.
  * States are by sequence (no slots).  Deterministic.  A value that is not finite
- * may spoil every gradient of its head in the same 16 tokens of its sequence.
+ * may spoil every gradient of its head in the same 16 tokens of its sequence, and
+ * with them dstate_in where the formula spoils a part of it.
  *
  * rq_tmix_step -- one token for each of B sequences: r .. b and y [B, H, 64],
  * states and slots as above.  B >= 1.
