@@ -34,8 +34,8 @@ namespace rq {
 namespace {
 
 constexpr int UNROLL = 4;                    // pairs
-constexpr int RPL = 1, NCW = 2;              // rows per lane, row warps of a CTA
-constexpr int ROWS = NCW * 4 * RPL;          // of a CTA: a head is spread over eight
+constexpr int NCW = 2;                       // row warps of a CTA
+constexpr int ROWS = NCW * 4;                // of a CTA: a head is spread over eight
 constexpr int CT = kTmixChunk;               // tokens staged at once
 constexpr int NPW = 4;                       // producer warps: a pair of tokens and 4 channels per thread
 static_assert(NPW * 32 == CT / 2 * kHead / 4);
@@ -188,35 +188,22 @@ __device__ __forceinline__ void stage_chunk(Stage<REV>& st, const Raw<T>& raw, i
     }
 }
 
-// Sums of N values over eight lanes (N a power of two, at most 8), each lane
-// keeping one of them: lane q has value q * N / 8.  Two sets at a time, so that
-// the shuffles of one pass while those of the other are on their way.
-template <int N, bool TWO>
-__device__ __forceinline__ void sum_lanes(float (&v)[N], float (&o)[N], int lane) {
-    int mask = 4;
+// Sums of two values over eight lanes: lanes 0 .. 3 keep the first (in v[0]), 4 .. 7
+// the second.  Two sets at a time, so that the shuffles of one pass while those of
+// the other are on their way.
+template <bool TWO>
+__device__ __forceinline__ void sum_lanes(float (&v)[2], float (&o)[2], int lane) {
+    const bool upper = lane & 4;
+    float give = upper ? v[0] : v[1], give2 = upper ? o[0] : o[1];
+    v[0] = upper ? v[1] : v[0];
+    if (TWO) o[0] = upper ? o[1] : o[0];
 #pragma unroll
-    for (int n = N / 2; mask >= 1; n /= 2, mask /= 2) {
-        const bool upper = lane & mask;
-        float give[N], give2[N];
-#pragma unroll
-        for (int i = 0; i < (n ? n : 1); ++i) {
-            give[i] = n ? (upper ? v[i] : v[i + n]) : v[0];
-            if (n) v[i] = upper ? v[i + n] : v[i];
-            if (TWO) {
-                give2[i] = n ? (upper ? o[i] : o[i + n]) : o[0];
-                if (n) o[i] = upper ? o[i + n] : o[i];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < (n ? n : 1); ++i) give[i] = __shfl_xor_sync(0xffffffffu, give[i], mask);
-#pragma unroll
-        for (int i = 0; i < (n ? n : 1); ++i) {
-            if (TWO) give2[i] = __shfl_xor_sync(0xffffffffu, give2[i], mask);
-            v[i] += give[i];
-        }
-#pragma unroll
-        for (int i = 0; i < (n ? n : 1); ++i)
-            if (TWO) o[i] += give2[i];
+    for (int mask = 4; mask >= 1; mask /= 2) {
+        if (mask < 4) give = v[0], give2 = o[0];
+        give = __shfl_xor_sync(0xffffffffu, give, mask);
+        if (TWO) give2 = __shfl_xor_sync(0xffffffffu, give2, mask);
+        v[0] += give;
+        if (TWO) o[0] += give2;
     }
 }
 
@@ -230,7 +217,7 @@ __device__ __forceinline__ void store_y(const TmixArgs& p, const float (*y)[ROWS
     }
 }
 
-// One CTA: NCW compute warps of 4 RPL rows each, of one head of one sequence.
+// One CTA: NCW compute warps of 4 rows each, of one head of one sequence.
 template <typename T, bool REV>
 __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_pairs_kernel(const TmixArgs p) {
     constexpr int SPLIT = kHead / ROWS;
@@ -281,32 +268,25 @@ __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_pairs_kernel(const Tmix
         return;
     }
 
-    // compute warps: lane (g, q) holds rows wrow .. wrow + RPL - 1, keys 4 q + 0..3 and 32 + 4 q + 0..3
-    const int q = lane & 7, wrow = (warp * 4 + (lane >> 3)) * RPL;
-    uint64_t S[RPL][4];
+    // compute warps: lane (g, q) holds keys 4 q + 0..3 and 32 + 4 q + 0..3 of row wrow
+    const int q = lane & 7, wrow = warp * 4 + (lane >> 3);
+    uint64_t S[4];
     const int64_t head_state = (slot * p.H + h) * kHead * kHead;
+    const int64_t mine = static_cast<int64_t>(row0 + wrow) * kHead + 4 * q;
 #pragma unroll
-    for (int r = 0; r < RPL; ++r) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p.state_in != nullptr && slot >= 0)
-                f = *reinterpret_cast<const float4*>(p.state_in + head_state + (row0 + wrow + r) * kHead + 32 * i +
-                                                     4 * q);
-            S[r][2 * i] = pack2(f.x, f.y);
-            S[r][2 * i + 1] = pack2(f.z, f.w);
-        }
+    for (int i = 0; i < 2; ++i) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.state_in != nullptr && slot >= 0)
+            f = *reinterpret_cast<const float4*>(p.state_in + head_state + mine + 32 * i);
+        S[2 * i] = pack2(f.x, f.y);
+        S[2 * i + 1] = pack2(f.z, f.w);
     }
     float* const ck = REV ? p.gckpt : p.ckpt;
     const auto store_state = [&](float* dst) {
 #pragma unroll
-        for (int r = 0; r < RPL; ++r) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 a = unpack2(S[r][2 * i]), b = unpack2(S[r][2 * i + 1]);
-                *reinterpret_cast<float4*>(dst + (row0 + wrow + r) * kHead + 32 * i + 4 * q) =
-                    make_float4(a.x, a.y, b.x, b.y);
-            }
+        for (int i = 0; i < 2; ++i) {
+            const float2 a = unpack2(S[2 * i]), b = unpack2(S[2 * i + 1]);
+            *reinterpret_cast<float4*>(dst + mine + 32 * i) = make_float4(a.x, a.y, b.x, b.y);
         }
     };
     struct Keys {
@@ -318,14 +298,12 @@ __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_pairs_kernel(const Tmix
         if (ck != nullptr) store_state(ck + ((ckpt_base(lo, seq) + ch) * p.H + h) * kHead * kHead);
         const Stage<REV>& st = sm.st[c & 1];
         // y of a pair is summed over the lanes while the next pair's products are on their way
-        float last[2 * RPL] = {};
+        float last[2] = {};
         const auto write_y = [&](int pair) {             // last[0]: this lane's sum
             const float out = last[0];
-            constexpr int STEP = 4 / RPL;
             // (as assembly: the compiler would let no load of the next pair pass a store to shared memory)
-            const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(
-                &sm.y[c & 1][2 * pair + q / STEP / RPL][wrow + q / STEP % RPL]));
-            if (q % STEP == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(out));
+            const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.y[c & 1][2 * pair + q / 4][wrow]));
+            if (q % 4 == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(out));
         };
 #pragma unroll UNROLL
         for (int n = 0; n < pairs; ++n) {
@@ -335,78 +313,49 @@ __global__ void __launch_bounds__((NCW + NPW) * 32) tmix_pairs_kernel(const Tmix
                 const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(f), y = *reinterpret_cast<const ulonglong2*>(f + 32);
                 return Keys{{x.x, x.y, y.x, y.y}};
             };
-            const auto dot = [&](const Keys& k, float* to) {
-#pragma unroll
-                for (int r = 0; r < RPL; ++r) {
-                    const float2 f = unpack2(add2(fma2(S[r][2], k.v[2], mul2(S[r][0], k.v[0])),
-                                                  fma2(S[r][3], k.v[3], mul2(S[r][1], k.v[1]))));
-                    to[r] = f.x + f.y;
-                }
+            const auto dot = [&](const Keys& k) {
+                const float2 f = unpack2(add2(fma2(S[2], k.v[2], mul2(S[0], k.v[0])), fma2(S[3], k.v[3], mul2(S[1], k.v[1]))));
+                return f.x + f.y;
             };
-            const auto add = [&](const Keys& k, const float* f) {
+            const auto add = [&](const Keys& k, float f) {
+                const uint64_t ff = pack2(f, f);
 #pragma unroll
-                for (int r = 0; r < RPL; ++r) {
-                    const uint64_t ff = pack2(f[r], f[r]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) S[r][i] = fma2(ff, k.v[i], S[r][i]);
-                }
+                for (int i = 0; i < 4; ++i) S[i] = fma2(ff, k.v[i], S[i]);
             };
-            float row1[RPL], row2[RPL];
-#pragma unroll
-            for (int r = 0; r < RPL; ++r) {
-                row1[r] = st.row[2 * pair][wrow + r];
-                row2[r] = st.row[2 * pair + 1][wrow + r];
-            }
+            const float row1 = st.row[2 * pair][wrow], row2 = st.row[2 * pair + 1][wrow];
             const float4 dots = st.dots[pair];
             // the two dot products of the update, summed over the lanes and back in all of them
-            float x[2 * RPL], u1[RPL], u2[RPL], y[2 * RPL];
-            dot(vec(1), x);
-            dot(vec(2), x + RPL);
-            if constexpr (!REV) dot(vec(3), y);
-            sum_lanes<2 * RPL, !REV>(x, last, lane);
-            const float mine = x[0];
-#pragma unroll
-            for (int r = 0; r < RPL; ++r) {
-                constexpr int STEP = 4 / RPL;            // lane of a value: 8 / (2 RPL) apart
-                u1[r] = __shfl_sync(0xffffffffu, mine, r * STEP, 8);
-                u2[r] = __shfl_sync(0xffffffffu, mine, (RPL + r) * STEP, 8);
-            }
+            float x[2] = {dot(vec(1)), dot(vec(2))}, y = 0.f;
+            if constexpr (!REV) y = dot(vec(3));
+            sum_lanes<!REV>(x, last, lane);
+            float u1 = __shfl_sync(0xffffffffu, x[0], 0, 8), u2 = __shfl_sync(0xffffffffu, x[0], 4, 8);
             if (!REV && n > 0) write_y(pair - 1);
             {
                 const Keys w = vec(0);
 #pragma unroll
-                for (int r = 0; r < RPL; ++r) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) S[r][i] = fma2(S[r][i], w.v[i], S[r][i]);
-                }
+                for (int i = 0; i < 4; ++i) S[i] = fma2(S[i], w.v[i], S[i]);
             }
             if constexpr (!REV) {
                 add(vec(5), row1);
                 add(vec(7), row2);
-#pragma unroll
-                for (int r = 0; r < RPL; ++r) {
-                    u2[r] = fmaf(row1[r], dots.y, fmaf(u1[r], dots.x, u2[r]));
-                    // once for the row: the sum over the lanes follows
-                    last[r] = q == 0 ? fmaf(row1[r], dots.w, fmaf(u1[r], dots.z, y[r])) : y[r];
-                }
+                u2 = fmaf(row1, dots.y, fmaf(u1, dots.x, u2));
+                // once for the row: the sum over the lanes follows
+                last[0] = q == 0 ? fmaf(row1, dots.w, fmaf(u1, dots.z, y)) : y;
                 add(vec(4), u1);
                 add(vec(6), u2);
-                dot(vec(8), last + RPL);
+                last[1] = dot(vec(8));
             } else {
                 add(vec(3), row2);
                 add(vec(5), row1);
                 // x: G b2 and G (w2 b1)
-#pragma unroll
-                for (int r = 0; r < RPL; ++r) {
-                    u1[r] = fmaf(row2[r], dots.x, u1[r]);
-                    u2[r] = fmaf(row1[r], dots.w, fmaf(u1[r], dots.z, fmaf(row2[r], dots.y, u2[r])));
-                }
+                u1 = fmaf(row2, dots.x, u1);
+                u2 = fmaf(row1, dots.w, fmaf(u1, dots.z, fmaf(row2, dots.y, u2)));
                 add(vec(4), u1);
                 add(vec(6), u2);
             }
         }
         if constexpr (!REV) {
-            sum_lanes<2 * RPL, false>(last, last, lane);
+            sum_lanes<false>(last, last, lane);
             write_y(pairs - 1);
         }
         __syncthreads();
