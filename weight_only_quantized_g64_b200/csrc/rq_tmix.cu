@@ -702,12 +702,13 @@ __global__ void __launch_bounds__(128) tmix_step_kernel(const TmixArgs p) {
 }  // namespace
 
 cudaError_t launch_tmix_scan(const TmixArgs& a, bool half, bool reverse, cudaStream_t s) {
-    // Up to a head (of all sequences together) for every four SMs, most SMs would be
-    // without one of this kernel's CTAs, and its first chunk takes 10 us; pairs of
-    // tokens split a head over eight CTAs.  Forwards + backwards in us, pairs /
-    // this kernel: 12 heads of 128 tokens 16 + 13 / 27 + 21, of 1024 101 + 81 / 180 +
-    // 150; 32 heads of 512 65 + 49 / 94 + 77; 64 of 512 96 + 78 / 97 + 78, of 1024
-    // (forwards) 185 / 173; 128 of 512 188 + 110 / 98 + 79.
+    // Up to a head (of all sequences together, empty ones too: their lengths are on the
+    // device) for every four SMs, most SMs would be without one of this kernel's CTAs,
+    // and its first chunk takes 10 us; pairs of tokens split a head over eight CTAs.
+    // Forwards and the gradients' call in us, one fp16 sequence, pairs / this kernel: 12
+    // heads of 128 tokens 19, 30 / 30, 38, of 1024 104, 128 / 176, 190; 37 of 1024 141, 247
+    // / 176, 262; 32 of 512 74, 112 / 93, 131; 40 of 512 101, 146 / 93, 145; 48 102, 159
+    // / 93, 159; 64 144, 198 / 93, 179; 128 256, 380 / 93, 271.
     if (static_cast<int64_t>(a.S) * a.H * 4 <= num_sms()) return launch_tmix_pairs(a, half, reverse, s);
     if (half) return reverse ? launch_scan<__half, true>(a, s) : launch_scan<__half, false>(a, s);
     return reverse ? launch_scan<float, true>(a, s) : launch_scan<float, false>(a, s);
