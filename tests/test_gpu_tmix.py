@@ -560,3 +560,59 @@ def test_gradient_of_strong_and_weak_decays():
     off = np.abs(grads[1].double().cpu().numpy() / ref - 1)
     lim = (92 + 6 * np.abs(d)) * 2.0 ** -24
     assert np.all(off <= lim), f"worst {(off / lim).max():.2f} of the bound at d = {d.flat[(off / lim).argmax()]}"
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_scan_of_many_heads_in_a_pool(dtype):
+    """States of a pool updated in place by the kernel for many heads; an empty sequence, and one without a state."""
+    H, starts = 30, [0, 40, 40, 57, 90]
+    T, S = starts[-1], len(starts) - 1
+    xs = inputs(T, H, dtype, seed=31)
+    pool = (0.3 * torch.randn((7, H, HEAD, HEAD), generator=torch.Generator().manual_seed(1))).cuda()
+    slots = [5, 2, -1, 0]
+    first = pool.clone()
+    y, out = rq.tmix_scan(*xs, torch.tensor(starts, dtype=torch.int32, device="cuda"), state=pool, state_out=pool,
+                          slots=torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    assert out is pool
+    state = torch.stack([first[s] if s >= 0 else torch.zeros_like(first[0]) for s in slots])
+    ref_y, ref_S = reference(xs, starts, state)
+    check(y, ref_y, "y")
+    for i, s in enumerate(slots):
+        if s >= 0:
+            check(pool[s], ref_S[i], "state")
+    assert torch.equal(pool[[1, 2, 3, 4, 6]], first[[1, 2, 3, 4, 6]])
+
+
+@pytest.mark.parametrize("name", ["r", "d", "k", "v", "a", "b", "dy"])
+@pytest.mark.parametrize("H", [2, 66])
+def test_non_finite_and_gradients(name, H):
+    """A NaN at token 21 of one head: outside its 16 tokens every gradient that the formula keeps finite keeps its
+    value, and so do the other head's and the other sequence's in full."""
+    starts, h = [0, 50, 70], 1
+    xs = inputs(70, H, torch.float32, seed=12)
+    dy = torch.randn((70, H, HEAD), generator=torch.Generator().manual_seed(3)).cuda()
+    dstate = torch.randn((2, H, HEAD, HEAD), generator=torch.Generator().manual_seed(4)).cuda()
+    seq = torch.tensor(starts, dtype=torch.int32, device="cuda")
+
+    def run():
+        ckpt = rq.tmix_ckpt(xs[0], 2)
+        rq.tmix_scan(*xs, seq, ckpt=ckpt)
+        return rq.tmix_scan_bwd(*xs, seq, ckpt, dy, dstate_out=dstate)
+
+    clean, clean_start = run()
+    (dy if name == "dy" else xs["rdkvab".index(name)])[21, h, 9] = float("nan")
+    got, start = run()
+    one = [x[:, h:h + 1] for x in xs]
+    _, _, ref, _ = reference(one, starts, None, dy[:, h:h + 1], dstate[:, h:h + 1])
+    rest = torch.ones(70, H, dtype=torch.bool)
+    rest[:50, h] = False
+    assert torch.equal(start[1], clean_start[1]) and torch.equal(start[0, [0]], clean_start[0, [0]])
+    for i, n in enumerate("rdkvab"):
+        assert torch.equal(got[i][rest.cuda()], clean[i][rest.cuda()]), n
+        values = ref[i].copy()
+        values[16:32] = np.nan               # (check leaves NaN of the formula out)
+        values[50:] = np.nan
+        live = ~np.isnan(values)
+        x = got[i][:, h:h + 1].double().cpu().numpy()
+        lim = (2 if n == "d" else 1) * 3e-5 * clean[i][:50, h].abs().max().item()
+        assert not live.any() or np.all(np.abs(x[live] - values[live]) <= lim), n
