@@ -63,7 +63,7 @@ struct alignas(16) Chunk {
     // W of the last token as x + y, applied as S x + S y: (W - 1, 1) above 1/2, where S W = S + S (W - 1) keeps W's
     // distance from 1 (W itself, rounded to 24 bits, would carry the same error into the state in every chunk), and
     // (W, 0) below, where W - 1 would lose W's own bits
-    float2 last[kHead];
+    float last[2][kHead];
     T v[C][kHead + 8];
     int bad;                                 // a value of the chunk is not finite
 };
@@ -206,7 +206,10 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
         a[j] *= prev;
         b[j] *= back;
         if (!REV) k[j] *= back;
-        if (token == C - 1) ch.last[k0 + j] = w[j] > -1.f ? make_float2(expm1_near(w[j] * kLn2), 1.f) : make_float2(W, 0.f);
+        if (token == C - 1) {
+            ch.last[0][k0 + j] = w[j] > -1.f ? expm1_near(w[j] * kLn2) : W;
+            ch.last[1][k0 + j] = w[j] > -1.f ? 1.f : 0.f;
+        }
     }
     put8(&sm.R[token][k0], r);
     put8(REV ? &ch.b[token][k0] : &sm.x[token][k0], a);
@@ -349,6 +352,21 @@ __device__ __forceinline__ void prepare(Group<T, REV>& sm, Chunk<T, REV>& ch, in
 // S[n][j]: row g (j < 2) or g + 8, key 8 n + 2 q + j % 2
 using State = float[8][4];
 
+__device__ __forceinline__ void decay(State& S, const float (&last)[2][kHead], int q) {
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const uint64_t x = *reinterpret_cast<const uint64_t*>(&last[0][8 * n + 2 * q]);
+        const uint64_t y = *reinterpret_cast<const uint64_t*>(&last[1][8 * n + 2 * q]);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const uint64_t s = pack2(S[n][i], S[n][i + 1]);
+            const float2 f = unpack2(fma2(s, x, mul2(s, y)));
+            S[n][i] = f.x;
+            S[n][i + 1] = f.y;
+        }
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ void forward_chunk(State& S, const Chunk<T, false>& ch, float (*y)[C + 4], int row, int lane) {
     const int g = lane >> 2, q = lane & 3;
@@ -407,14 +425,7 @@ __device__ __forceinline__ void forward_chunk(State& S, const Chunk<T, false>& c
 #pragma unroll
             for (int j = 0; j < 4; ++j) S[n + i][j] += d.at(i, j);
     }
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-        const float4 w = *reinterpret_cast<const float4*>(&ch.last[8 * n + 2 * q]);
-        S[n][0] = fmaf(S[n][0], w.x, S[n][0] * w.y);
-        S[n][1] = fmaf(S[n][1], w.z, S[n][1] * w.w);
-        S[n][2] = fmaf(S[n][2], w.x, S[n][2] * w.y);
-        S[n][3] = fmaf(S[n][3], w.z, S[n][3] * w.w);
-    }
+    decay(S, ch.last, q);
     if (__any_sync(0xffffffffu, min(from[0], from[1]) < C)) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -478,14 +489,7 @@ __device__ __forceinline__ void forward_tokens(State& S, const Chunk<T, false>& 
 template <typename T>
 __device__ __forceinline__ void backward_chunk(State& G, const Chunk<T, true>& ch, int row, int lane) {
     const int g = lane >> 2, q = lane & 3;
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-        const float4 w = *reinterpret_cast<const float4*>(&ch.last[8 * n + 2 * q]);
-        G[n][0] = fmaf(G[n][0], w.x, G[n][0] * w.y);
-        G[n][1] = fmaf(G[n][1], w.z, G[n][1] * w.w);
-        G[n][2] = fmaf(G[n][2], w.x, G[n][2] * w.y);
-        G[n][3] = fmaf(G[n][3], w.z, G[n][3] * w.w);
-    }
+    decay(G, ch.last, q);
     Sums<2> X;
     X.clear();
 #pragma unroll
