@@ -329,9 +329,8 @@ rq_status rq_gemm_wq(const uint16_t *x, int64_t M, int64_t K, const void *codes,
 
 /*
  * rq_lora_add -- low-rank adapters of many requests beside a shared projection
- * (the weight is quantized and shared; the adapters stay fp16, as the model
- * card keeps its low-rank matrices in full precision, "Format & loading
- * (important)").  For every token m with a = ids[m]:
+ * (the weight is quantized and shared; the adapters stay fp16.  The pages have
+ * no such call).  For every token m with a = ids[m]:
  *   out[m, n] = epi( y[m, n] + scale[a] * sum_{r < ranks[a]} B[a, n, r] t[r] ),
  *   t[r] = sum_k A[a, r, k] x[m, k];
  * a token with a negative id has no adapter: out[m, n] = epi(y[m, n]); an id

@@ -20,8 +20,8 @@
 //
 // About 204 + 87 MMAs per warp and chunk (rq_tf32.cuh), 8 cycles each, bound the
 // kernel from below: 2300 cycles a chunk.  It takes 5000 (64 heads of 1024 tokens:
-// the row warps by themselves 107 us, the preparing warps by themselves 128,
-// together 172): both sides are chains of dependent products and share the issue
+// the row warps by themselves 104 us, the preparing warps by themselves 137,
+// together 176): both sides are chains of dependent products and share the issue
 // slots.  (Two CTAs per head that prepare for one another through distributed
 // shared memory: 4500 cycles with four preparing groups, and more where other heads
 // wait for an SM.)  Plain fp32 FMAs over pairs of tokens (rq_tmix_pairs.cu, which

@@ -21,7 +21,7 @@
 // About 800 000 multiplications per chunk and head, on the tensor cores
 // (rq_tf32.cuh): 2300 MMAs of 8 cycles over the four of an SM bound it.  With
 // plain FMAs the kernel was bound by shared-memory reads at 4 x 4 results per
-// thread: 322 us where this takes 200 (2048 tokens, 32 heads, fp16).
+// thread: 322 us where this takes 197 (2048 tokens, 32 heads, fp16).
 // The loops over the summed index are not unrolled: the code of all products is
 // what the instruction cache holds least of (steps of 2 together 205 us, all 268).
 // A value that is not finite may spoil the gradients of its chunk of 16 tokens.
